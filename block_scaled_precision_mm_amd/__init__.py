@@ -20,6 +20,17 @@ fall back to another implementation).  There is no CPU fallback: if the
 library is missing, importing this package raises.
 
 ``scaled_mm`` is the convenience form that allocates C and returns it.
+
+Around the products (see the same header):
+
+    mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, stream=None)
+    KVCache(k_codes, k_scales, v_codes, v_scales, fmt), KVCache.empty(pages, page_size, kv_heads, head_dim, fmt)
+    mx_kv_cache_write(cache, k, v, slots, stream=None)
+    mx_kv_cache_read(cache, k, v, slots, stream=None)
+    mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, causal=True, window=0,
+                       max_new=None, workspace="auto", stream=None)
+
+``rmsnorm`` and ``paged_attention`` are their convenience forms.
 """
 from __future__ import annotations
 
@@ -76,7 +87,14 @@ _lib.mx_fused_variant_max_k.argtypes = [_INT, _INT]
 _lib.mx_fused_variant_max_k.restype = _I64
 _lib.mx_dense_gemm.argtypes = [_INT, _INT, _INT, _P, _P, _P, _I64, _I64, _I64, _INT, _P]
 _lib.mx_empty_like.argtypes = [_INT, _I64, _I64, _I64, _P]
-for _f in ("mx_scaled_mm_fp4", "mx_scaled_mm_fp8", "mx_scaled_mm_config", "mx_num_variants",
+_lib.mx_rmsnorm.argtypes = [_P, _P, _P, _P, _P, _P, _I64, _I64, ctypes.c_float, _INT, _P]
+_lib.mx_kv_cache_write.argtypes = [_P, _P, _P, _I64, _I64, _P, _I64, _P]
+_lib.mx_kv_cache_read.argtypes = _lib.mx_kv_cache_write.argtypes
+_lib.mx_paged_attention.argtypes = [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, ctypes.c_float,
+                                    _INT, _I64, _P, _INT, _P, _P, _SZ, _P]
+_lib.mx_paged_attention_workspace_bytes.argtypes = [_P, _I64, _I64, _I64, _I64]
+_lib.mx_paged_attention_workspace_bytes.restype = _SZ
+for _f in ("mx_rmsnorm", "mx_kv_cache_write", "mx_kv_cache_read", "mx_paged_attention", "mx_scaled_mm_fp4", "mx_scaled_mm_fp8", "mx_scaled_mm_config", "mx_num_variants",
            "mx_default_config", "mx_scaled_mm_noalloc",
            "mx_last_hip_error", "mx_abi_version", "mx_default_variant", "mx_quantize_bf16",
            "mx_grouped_mm_fp4", "mx_grouped_mm_fp8", "mx_grouped_mm_config",
@@ -93,7 +111,9 @@ EXPORTS = ("mx_scaled_mm_fp4", "mx_scaled_mm_fp8", "mx_scaled_mm_config", "mx_nu
            "mx_grouped_mm_fp4", "mx_grouped_mm_fp8", "mx_grouped_mm_config",
            "mx_grouped_num_variants", "mx_grouped_variant_name", "mx_grouped_default_variant",
            "mx_scaled_mm_fused", "mx_fused_num_variants", "mx_fused_variant_name",
-           "mx_fused_default_variant", "mx_fused_variant_max_k", "mx_dense_gemm", "mx_empty_like")
+           "mx_fused_default_variant", "mx_fused_variant_max_k", "mx_dense_gemm", "mx_empty_like",
+           "mx_rmsnorm", "mx_kv_cache_write", "mx_kv_cache_read", "mx_paged_attention",
+           "mx_paged_attention_workspace_bytes")
 
 
 class MxGemmError(RuntimeError):
@@ -488,3 +508,185 @@ def mx_scaled_mm_noalloc(is_fp4, a, b, a_scale, b_scale, c, M, N, K, out_dtype=N
 
 def mx_noalloc_scratch_bytes() -> int:
     return int(_lib.mx_noalloc_scratch_bytes())
+
+
+# ------------------------------------------------- around the products
+def mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, stream=None) -> None:
+    """RMSNorm with the residual's addition (C ABI mx_rmsnorm): x, residual
+    (or None) and h (or None) bfloat16 [rows][K], weight bfloat16 [K] or None.
+    y: the output in its own dtype (BF16 / FP16 / FP32), or 1-byte E4M3 codes
+    [rows][K] or E2M1 pairs [rows][K/2] with y_scale uint8 [rows][K/32]; a
+    1-byte y takes its format from its size unless out_kind is given."""
+    n = rows * K
+    for name, t in (("x", x), ("residual", residual), ("h", h)):
+        if isinstance(t, torch.Tensor):
+            if not t.is_cuda or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.numel() != n:
+                raise ValueError("%s must be a contiguous bfloat16 CUDA tensor of rows*K elements" % name)
+    if isinstance(weight, torch.Tensor):
+        if not weight.is_cuda or weight.dtype != torch.bfloat16 or not weight.is_contiguous() or weight.numel() != K:
+            raise ValueError("weight must be a contiguous bfloat16 CUDA tensor of K elements")
+    if out_kind is None:
+        if not isinstance(y, torch.Tensor):
+            raise ValueError("out_kind is required when y is a raw pointer")
+        out_kind = _OUT_OF_DTYPE.get(y.dtype)
+        if out_kind is None:
+            out_kind = OUT_MXFP8 if y.numel() == n else OUT_MXFP4
+    if isinstance(y, torch.Tensor):
+        m, size = {OUT_BF16: (n, 2), OUT_F16: (n, 2), OUT_F32: (n, 4), OUT_MXFP4: (n // 2, 1)}.get(out_kind, (n, 1))
+        if not y.is_cuda or not y.is_contiguous() or y.numel() != m or y.element_size() != size:
+            raise ValueError("y must be a contiguous CUDA tensor of %d elements of %d bytes" % (m, size))
+    if isinstance(y_scale, torch.Tensor):
+        if not y_scale.is_cuda or not y_scale.is_contiguous() or y_scale.element_size() != 1 or \
+                y_scale.numel() != rows * (K // 32):
+            raise ValueError("y_scale must be a contiguous 1-byte CUDA tensor of rows*K/32 elements")
+    st = _lib.mx_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y), _ptr(y_scale), rows, K, eps,
+                         out_kind, _stream(stream))
+    if st:
+        raise MxGemmError(st, "mx_rmsnorm")
+
+
+def rmsnorm(x, weight, residual=None, eps=1e-6, out="fp8", stream=None):
+    """(y, y_scale, h) of mx_rmsnorm on bfloat16 [..., K] tensors: out 'fp8'
+    or 'fp4' (codes and E8M0 scales, uint8) or a torch dtype (y_scale None);
+    h the sum with the residual (x itself without one)."""
+    K = x.shape[-1]
+    rows = x.numel() // K if K else 0
+    lead = x.shape[:-1]
+    h = torch.empty_like(x) if residual is not None else None
+    ys = None
+    if out in ("fp8", "fp4"):
+        y = torch.empty(lead + (K if out == "fp8" else K // 2,), dtype=torch.uint8, device=x.device)
+        ys = torch.empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
+        kind = OUT_MXFP8 if out == "fp8" else OUT_MXFP4
+    else:
+        y = torch.empty(x.shape, dtype=out, device=x.device)
+        kind = _OUT_OF_DTYPE[out]
+    mx_rmsnorm(x, residual, weight, h, y, ys, rows, K, eps, out_kind=kind, stream=stream)
+    return y, ys, x if residual is None else h
+
+
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("pages", _I64),
+                ("page_size", _I64), ("kv_heads", _I64), ("head_dim", _I64), ("is_fp4", _INT)]
+
+
+class KVCache:
+    """A paged key/value cache in MX formats (C ABI mxg_kv_cache_t): codes
+    [pages][kv_heads][page_size][head_dim] E4M3 bytes (fmt 'fp8') or
+    [..][head_dim/2] E2M1 pairs ('fp4'), scales [..][head_dim/32] E8M0 bytes."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "fmt", "pages", "page_size", "kv_heads", "head_dim",
+                 "_struct", "_ref")
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, fmt="fp8"):
+        if fmt not in ("fp4", "fp8"):
+            raise ValueError("fmt must be 'fp4' or 'fp8'")
+        if k_codes.dim() != 4:
+            raise ValueError("codes must be [pages][kv_heads][page_size][bytes of a row]")
+        pages, heads, size, row = (int(n) for n in k_codes.shape)
+        dim = row * 2 if fmt == "fp4" else row
+        for name, t, last in (("k_codes", k_codes, row), ("k_scales", k_scales, dim // 32),
+                              ("v_codes", v_codes, row), ("v_scales", v_scales, dim // 32)):
+            if not t.is_cuda or not t.is_contiguous() or t.element_size() != 1 or \
+                    tuple(t.shape) != (pages, heads, size, last):
+                raise ValueError("%s must be a contiguous 1-byte CUDA tensor [%d][%d][%d][%d]"
+                                 % (name, pages, heads, size, last))
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.fmt = k_codes, k_scales, v_codes, v_scales, fmt
+        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, dim
+        self._struct = _KVCacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                      v_scales.data_ptr(), pages, size, heads, dim, int(fmt == "fp4"))
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, pages, page_size, kv_heads, head_dim, fmt="fp8", device="cuda"):
+        """A cache whose slots hold zeros."""
+        row = head_dim // 2 if fmt == "fp4" else head_dim
+        shape = (pages, kv_heads, page_size)
+        t = [torch.zeros(shape + (n,), dtype=torch.uint8, device=device) for n in (row, head_dim // 32) * 2]
+        return cls(*t, fmt=fmt)
+
+
+def _token_rows(name, t, tokens, heads, dim):
+    """Stride between the tokens of a bfloat16 [tokens][heads][dim] tensor
+    whose tokens may be apart (a part of the rows of a joint product)."""
+    if not t.is_cuda or t.dtype != torch.bfloat16 or t.shape != (tokens, heads, dim) or \
+            (t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim))):
+        raise ValueError("%s must be a bfloat16 CUDA tensor [%d][%d][%d], each token's values contiguous"
+                         % (name, tokens, heads, dim))
+    return t.stride(0) if tokens > 1 else heads * dim
+
+
+def _cache_call(fn, name, cache, k, v, slots, stream):
+    if not slots.is_cuda or slots.dtype != torch.int64 or not slots.is_contiguous() or slots.dim() != 1:
+        raise ValueError("slots must be a contiguous one-dimensional int64 CUDA tensor")
+    n = slots.shape[0]
+    ks = _token_rows("k", k, n, cache.kv_heads, cache.head_dim)
+    vs = _token_rows("v", v, n, cache.kv_heads, cache.head_dim)
+    st = fn(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), n, _stream(stream))
+    if st:
+        raise MxGemmError(st, name)
+
+
+def mx_kv_cache_write(cache, k, v, slots, stream=None) -> None:
+    """Quantize tokens into cache slots (C ABI mx_kv_cache_write): k and v
+    bfloat16 [tokens][kv_heads][head_dim], tokens may be apart; slots int64
+    [tokens], -1 to skip one."""
+    _cache_call(_lib.mx_kv_cache_write, "mx_kv_cache_write", cache, k, v, slots, stream)
+
+
+def mx_kv_cache_read(cache, k, v, slots, stream=None) -> None:
+    """Read cache slots back (C ABI mx_kv_cache_read) into k and v, laid out
+    as for mx_kv_cache_write; a slot outside the cache reads zeros."""
+    _cache_call(_lib.mx_kv_cache_read, "mx_kv_cache_read", cache, k, v, slots, stream)
+
+
+def mx_paged_attention_workspace_bytes(cache, seqs, tokens, q_heads, max_new) -> int:
+    return int(_lib.mx_paged_attention_workspace_bytes(cache._ref, seqs, tokens, q_heads, max_new))
+
+
+def _int32(name, t, shape):
+    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.shape != shape:
+        raise ValueError("%s must be a contiguous int32 CUDA tensor of shape %s" % (name, tuple(shape)))
+
+
+def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, causal=True, window=0,
+                       max_new=None, workspace="auto", stream=None) -> None:
+    """Attention of new tokens over the paged cache (C ABI
+    mx_paged_attention): q bfloat16 [tokens][q_heads][head_dim], tokens may be
+    apart; ends and lens int32 [seqs]; table int32 [seqs][pages of a
+    sequence]; out contiguous [tokens][q_heads][head_dim] in BF16 / FP16 /
+    FP32; lse float32 [tokens][q_heads] or None.  scale: 1/sqrt(head_dim) if
+    None; max_new: the most new tokens of a sequence, if known (for speed)."""
+    tokens, heads, dim = q.shape
+    seqs = ends.shape[0]
+    if dim != cache.head_dim:
+        raise ValueError("q has head_dim %d, the cache %d" % (dim, cache.head_dim))
+    qs = _token_rows("q", q, tokens, heads, dim)
+    _int32("ends", ends, (seqs,))
+    _int32("lens", lens, (seqs,))
+    if table.dim() != 2:
+        raise ValueError("table must be [seqs][pages of a sequence]")
+    _int32("table", table, (seqs, table.shape[1]))
+    if not out.is_cuda or not out.is_contiguous() or out.shape != q.shape or out.dtype not in _OUT_OF_DTYPE:
+        raise ValueError("out must be a contiguous CUDA tensor of q's shape in BF16, FP16 or FP32")
+    if lse is not None and (not lse.is_cuda or lse.dtype != torch.float32 or not lse.is_contiguous() or
+                            lse.shape != (tokens, heads)):
+        raise ValueError("lse must be a contiguous float32 CUDA tensor [tokens][q_heads]")
+    if max_new is None:
+        max_new = tokens
+    st_ptr = _stream(stream)
+    need = _lib.mx_paged_attention_workspace_bytes(cache._ref, seqs, tokens, heads, max_new) if workspace is not None else 0
+    wp, wb = _workspace(workspace, need, st_ptr)
+    st = _lib.mx_paged_attention(cache._ref, q.data_ptr(), qs, ends.data_ptr(), lens.data_ptr(), table.data_ptr(),
+                                 table.shape[1], seqs, tokens, heads, max_new,
+                                 dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
+                                 _OUT_OF_DTYPE[out.dtype], 0 if lse is None else lse.data_ptr(), wp, wb, st_ptr)
+    if st:
+        raise MxGemmError(st, "mx_paged_attention")
+
+
+def paged_attention(cache, q, ends, lens, table, out_dtype=torch.bfloat16, **kw) -> torch.Tensor:
+    """mx_paged_attention into a new tensor, which it returns."""
+    out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    mx_paged_attention(cache, q, ends, lens, table, out, **kw)
+    return out

@@ -1,0 +1,1091 @@
+// mx_attn.hpp -- attention of each sequence's new tokens over the paged MX
+// key/value cache (mx_cache.hpp), gfx950.
+//
+// For query row (token, head) of a sequence with n new tokens and L keys, the
+// token at position pos = L - n + i:
+//     x_j  = scale * q . k_j          over the keys j it sees
+//     out  = sum_j exp(x_j) v_j / sum_j exp(x_j),   lse = log sum_j exp(x_j)
+// in one pass over the keys with a running maximum: the sums are kept
+// relative to a reference m, p_j = 2^(x_j log2 e - m).  A row that sees no key
+// gives 0 and lse = -inf.
+//
+// Types.  Codes are expanded to BF16 on the way into LDS (exactly: an E4M3 or
+// E2M1 element times a power of two has at most 4 significant bits), both
+// products run on the BF16 MFMA with FP32 accumulation, q.k of the given BF16
+// q is exact but for the accumulation, x, m and the sums are FP32.  p is
+// rounded to BF16 as the second product's operand (half a step: 2^-9 of each
+// p); the sum of the p's takes them unrounded.
+//
+// The rows of one KV head.  All G = q_heads / kv_heads query heads of a KV
+// head read the same keys, so a tile's rows are (token, head of the group)
+// pairs, token-major: keys are read and expanded once for the group, and a
+// short chunk fills the MFMA's rows with heads.
+//
+// Transposed products.  S^T = K Q^T and O^T = V^T P^T: a lane of the
+// accumulators holds one query row and several keys, so the softmax runs
+// inside lanes plus an exchange between the lanes of a row, rescaling O is a
+// multiplication by a lane's own factor, and P^T is already in the layout
+// of the second product's operand: the contraction over keys may take them
+// in any order, and V^T is read in the order in which S^T left them (two
+// transposing LDS reads of four keys each).
+//
+// Rescaling.  m is raised only when a row's maximum passes it by more than
+// 2^8 (a wave-uniform branch): until then p <= 256 relative to m, which FP32
+// sums and BF16's relative precision do not notice.
+//
+// Work (plan_item).  Sequence lengths are known on the device only.  A launch
+// has as many workgroups as can run at once plus one per (sequence, head,
+// row tile); each finds its own item from the lengths: key ranges longer
+// than the average work per resident workgroup are split, and the parts of
+// one row tile joined through a workspace by the workgroup that arrives
+// last, in part order (as mx_splitk.hpp does), so results do not depend on
+// timing.
+//
+// Masked places.  Scores of unseen keys are replaced, never added to;
+// values of slots past the sequence's end or on pages outside the cache are
+// replaced by zeros as they are expanded.  A NaN among the values of a key
+// that some rows of a tile see and others do not would reach the others as
+// 0 * NaN: such a tile (rare; found as it is expanded) runs its second
+// product on the values without the NaNs, and again on their indicator to
+// poison exactly the rows that see them.
+#pragma once
+
+#include "mx_cache.hpp"
+#include "mx_splitk.hpp"
+#include "mx_sync.hpp"
+
+namespace mxg {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
+typedef short s16x4v __attribute__((ext_vector_type(4)));
+
+struct AttnArgs {
+    const uint8_t *codes[2], *scales[2];    // keys, values
+    const uint16_t *q;                      // [tokens][q_heads][dim], q_stride elements between tokens
+    const int *ends, *lens, *table;
+    void *out;                              // [tokens][q_heads][dim]
+    float *lse;                             // [tokens][q_heads] or null
+    unsigned *counters;                     // one per row tile; null: no splitting
+    uint8_t *parts;                         // partial results of split row tiles
+    long long q_stride, table_stride;
+    float c;                                // scale * log2 e
+    int seqs, tokens, heads, group;         // KV heads, query heads per KV head
+    int page_shift, pages, table_width;
+    int causal, window;
+    int out_kind;
+    int rows_above, rows_upto;              // the sequences of this launch: rows_above < n * group <= rows_upto
+    int target;                             // resident workgroups
+};
+
+// One workgroup's work.
+struct AttnItem {
+    int seq, head, tok0, ntok, len;         // first row of q, new tokens, keys
+    int row0;                               // first row of the tile among ntok * group
+    int key0, key1;                         // its keys (key0 a multiple of BN)
+    int all_lo, all_hi;                     // keys that every row of the tile sees
+    int part, parts, slot, slot_step;       // split row tiles: this part, their number, workspace slots
+    int counter;
+};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A sequence as lane l of chunk c0 sees it: row tiles and key tiles of the
+// sequences of this launch's class, 0 row tiles for others.
+struct AttnSeq {
+    int tok0, ntok, len, rtiles, ktiles;
+};
+
+// carry: the end of the sequences before s - lane, updated to that of the 64.
+// Ends are taken as min(tokens, max(0, ends[0 .. s])), as group ends are
+// (mx_group.hpp), so the sequences' rows never overlap whatever they hold.
+template <int BM, int BN>
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &p, int s, int &carry)
+{
+    const int lane = threadIdx.x & 63;
+    AttnSeq q = {0, 0, 0, 0, 0};
+    int end = carry;
+    if (s < p.seqs) {
+        end = min(max(p.ends[s], carry), p.tokens);
+        const long long most = (long long)p.table_width << p.page_shift;
+        q.len = (int)min((long long)max(p.lens[s], 0), most);
+    }
+    int before = __shfl_up(end, 1);
+    before = lane ? before : carry;
+    const bool mine = s < p.seqs;
+    if (__any(mine && end < before)) {
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int u = __shfl_up(end, d);
+            end = lane >= d ? max(end, u) : end;
+        }
+        before = __shfl_up(end, 1);
+        before = lane ? before : carry;
+    }
+    carry = uniform(__shfl(end, 63));
+    q.tok0 = before;
+    q.ntok = mine ? end - before : 0;
+    const int rows = q.ntok * p.group;
+    if (rows > p.rows_above && rows <= p.rows_upto) {
+        q.rtiles = (rows + BM - 1) / BM;
+        // (with a window the keys before the first token's are not read)
+        const int lo = p.window > 0 ? max(0, q.len - q.ntok - p.window + 1) : 0;
+        q.ktiles = (q.len + BN - 1) / BN - min(lo, q.len) / BN;
+    }
+    return q;
+}
+
+template <class T>
+__device__ __forceinline__ T wave_sum(T v)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        v += __shfl_xor(v, d);
+    return v;
+}
+
+__device__ __forceinline__ int wave_prefix(int v)   // inclusive
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int u = __shfl_up(v, d);
+        v += lane >= d ? u : 0;
+    }
+    return v;
+}
+
+// Find workgroup `blockIdx.x`'s item; false if it has none.  Every wave of
+// the workgroup computes it (all results are wave-uniform).  min_tiles: the
+// fewest key tiles worth a part of their own.
+template <int BM, int BN>
+__device__ __forceinline__ bool plan_item(const AttnArgs &p, int min_tiles, AttnItem &it)
+{
+    const int lane = threadIdx.x & 63;
+    int chunk = 0x7FFFFFFF, carry = 0;
+    AttnSeq q = attn_seq<BM, BN>(p, lane, carry);
+    const int carry64 = carry;
+    if (p.counters) {
+        long long total = (long long)q.rtiles * q.ktiles;
+        for (int s0 = 64; s0 < p.seqs; s0 += 64) {
+            const AttnSeq r = attn_seq<BM, BN>(p, s0 + lane, carry);
+            total += (long long)r.rtiles * r.ktiles;
+        }
+        total = wave_sum(total) * p.heads;
+        const long long c = (total + p.target - 1) / p.target;
+        chunk = (int)min(max(c, (long long)min_tiles), (long long)0x7FFFFFFF);
+        chunk = uniform(chunk);
+    }
+    carry = carry64;
+    int item = blockIdx.x, slots = 0, tiles = 0;      // before the chunk of sequences looked at
+    for (int s0 = 0;; s0 += 64) {
+        if (s0 >= p.seqs)
+            return false;
+        if (s0 > 0)
+            q = attn_seq<BM, BN>(p, s0 + lane, carry);
+        const int parts = max(1, q.ktiles / chunk + (q.ktiles % chunk != 0));
+        const int mytiles = p.heads * q.rtiles, mine = mytiles * parts;
+        const int upto = wave_prefix(mine);
+        const int all = uniform(__shfl(upto, 63));
+        if (item >= all) {
+            item -= all;
+            slots += uniform(wave_sum(parts > 1 ? mine : 0));
+            tiles += uniform(wave_sum(mytiles));
+            continue;
+        }
+        const int at = __ffsll((unsigned long long)__ballot(item < upto)) - 1;
+        const int before_slots = wave_sum(lane < at && parts > 1 ? mine : 0);
+        const int before_tiles = wave_sum(lane < at ? mytiles : 0);
+        it.seq = s0 + at;
+        it.tok0 = uniform(__shfl(q.tok0, at));
+        it.ntok = uniform(__shfl(q.ntok, at));
+        it.len = uniform(__shfl(q.len, at));
+        const int rtiles = uniform(__shfl(q.rtiles, at)), sparts = uniform(__shfl(parts, at));
+        item -= uniform(__shfl(upto - mine, at));
+        // heads innermost: the workgroups of a head, which share its keys,
+        // are then apart by the number of heads and (with 8) on one XCD
+        it.head = item % p.heads;
+        const int rest = item / p.heads;
+        // the last row tiles of a causal chunk see the most keys: first
+        const int rt = rtiles - 1 - rest % rtiles;
+        it.part = rest / rtiles;
+        it.row0 = rt * BM;
+        it.counter = tiles + uniform(before_tiles) + rt * p.heads + it.head;
+        it.slot = slots + uniform(before_slots) + rt * p.heads + it.head;
+        it.slot_step = rtiles * p.heads;
+        // the keys that some row of the tile sees
+        const int t0 = it.row0 / p.group, t1 = min((it.row0 + BM - 1) / p.group, it.ntok - 1);
+        const int pos0 = it.len - it.ntok + t0, pos1 = it.len - it.ntok + t1;
+        const int hi = p.causal ? min(max(pos1 + 1, 0), it.len) : it.len;
+        const int lo = p.window > 0 ? min(max(pos0 - p.window + 1, 0), hi) : 0;
+        it.all_lo = p.window > 0 ? max(pos1 - p.window + 1, 0) : 0;
+        it.all_hi = p.causal ? min(max(pos0 + 1, 0), it.len) : it.len;
+        const int k0 = lo / BN, nt = (hi + BN - 1) / BN - k0;
+        it.parts = min(sparts, max(1, nt / chunk + (nt % chunk != 0)));
+        if (it.part >= it.parts)
+            return false;
+        it.key0 = (k0 + (int)((long long)nt * it.part / it.parts)) * BN;
+        it.key1 = min(hi, (k0 + (int)((long long)nt * (it.part + 1) / it.parts)) * BN);
+        return true;
+    }
+}
+
+// What one query row sees: keys [lo, hi).
+struct AttnRow {
+    int lo, hi;
+    int token, head;        // token of the sequence, head of the group; token < 0: no such row
+};
+
+__device__ __forceinline__ AttnRow attn_row(const AttnArgs &p, const AttnItem &it, int row)
+{
+    AttnRow r;
+    const int token = row / p.group;
+    r.head = row - token * p.group;
+    r.token = token < it.ntok ? token : -1;
+    const int pos = it.len - it.ntok + token;
+    r.hi = token < it.ntok ? (p.causal ? min(max(pos + 1, 0), it.len) : it.len) : 0;
+    r.lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+    return r;
+}
+
+// Geometry of KT keys of codes, loaded 16 bytes per lane by NTHR threads:
+// CH chunks per key, chunk (tid % CH) of key tid / CH + j * KPL in load j
+// (threads from KPL * CH on load nothing).
+template <int F, int D, int KT, int NTHR>
+struct AttnGeom {
+    static constexpr int RB = F == FMT_FP4 ? D / 2 : D;     // bytes of a key's codes
+    static constexpr int SB = D / 32;                       // and of its scales
+    static constexpr int CH = RB / 16;
+    static constexpr int VC = F == FMT_FP4 ? 32 : 16;       // values of a chunk
+    static constexpr int KPL = NTHR / CH < KT ? NTHR / CH : KT;   // keys per load
+    static constexpr bool ALL = KPL * CH == NTHR;           // every thread loads
+    static constexpr int NL = KT / KPL;                     // loads per thread
+    static_assert(KT % KPL == 0 && NL >= 1, "whole loads");
+};
+
+// Codes, scale codes and validity of this thread's chunks of a tile of keys.
+template <class G>
+struct AttnTileRegs {
+    u4v k[G::NL], v[G::NL];
+    unsigned ks[G::NL], vs[G::NL];      // scale code of the chunk
+    bool ok[G::NL];
+};
+
+// Page of key `key` of a sequence (its table row), or -1 past key1 or where
+// the table names no page of the cache.
+__device__ __forceinline__ int attn_page(const AttnArgs &p, const int *table, int key, int key1)
+{
+    int page = -1;
+    if (key < key1)
+        page = table[key >> p.page_shift];
+    return (unsigned)page < (unsigned)p.pages ? page : -1;
+}
+
+// Row of the cache (codes and scales) of key `key` on page `page`.  A key
+// that is not there (page < 0) takes row 0: in bounds, and not used.
+__device__ __forceinline__ long long attn_row_at(const AttnArgs &p, int page, int head, int key)
+{
+    const int off = key & ((1 << p.page_shift) - 1);
+    return page >= 0 ? ((((long long)page * p.heads + head) << p.page_shift) + off) : 0;
+}
+
+template <class G>
+__device__ __forceinline__ void attn_load(const AttnArgs &p, int head, int key, int chunk, const int (&page)[G::NL],
+                                          AttnTileRegs<G> &r)
+{
+#pragma unroll
+    for (int j = 0; j < G::NL; ++j) {
+        r.ok[j] = page[j] >= 0;
+        const long long at = attn_row_at(p, page[j], head, key + j * G::KPL);
+        r.k[j] = *reinterpret_cast<const u4v *>(p.codes[0] + at * G::RB + 16 * chunk);
+        r.v[j] = *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + 16 * chunk);
+        r.ks[j] = p.scales[0][at * G::SB + chunk * G::VC / 32];
+        r.vs[j] = p.scales[1][at * G::SB + chunk * G::VC / 32];
+    }
+}
+
+// A chunk as BF16: VC / 8 pieces of eight values.
+template <int F, int NP>
+__device__ __forceinline__ void attn_expand(const u4v &c, unsigned s, u4v (&w)[NP])
+{
+    if constexpr (F == FMT_FP4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = mx_decode8<F>(u2v{c[i], 0u}, s);
+    } else {
+        w[0] = mx_decode8<F>(u2v{c[0], c[1]}, s);
+        w[1] = mx_decode8<F>(u2v{c[2], c[3]}, s);
+    }
+}
+
+// Whether a chunk holds a NaN.
+template <int F>
+__device__ __forceinline__ bool attn_has_nan(const u4v &c, unsigned s)
+{
+    bool nan = s == 255u;
+    if constexpr (F == FMT_FP8) {
+        unsigned t = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t |= (c[i] & 0x7F7F7F7Fu) + 0x01010101u;
+        nan |= (t & 0x80808080u) != 0;
+    }
+    return nan;
+}
+
+enum { VALUES_PLAIN = 0, VALUES_CLEAN = 1, VALUES_NAN = 2 };   // as they are; NaNs as 0; 1 at NaNs, else 0
+
+__device__ __forceinline__ unsigned bf16_pair_mode(unsigned w, int mode)
+{
+    unsigned o = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const unsigned x = (w >> (16 * h)) & 0xFFFFu;
+        const bool nan = (x & 0x7FFFu) > 0x7F80u;
+        o |= (mode == VALUES_CLEAN ? (nan ? 0u : x) : (nan ? 0x3F80u : 0u)) << (16 * h);
+    }
+    return o;
+}
+
+// A piece of a key's values as the second product takes it: zeros for a key
+// that is not there.
+__device__ __forceinline__ u4v values_mode(u4v w, bool ok, int mode)
+{
+    if (mode != VALUES_PLAIN) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = bf16_pair_mode(w[i], mode);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = ok ? w[i] : 0u;
+    return w;
+}
+
+__device__ __forceinline__ bf16x8v as_bf16x8(u4v v) { return __builtin_bit_cast(bf16x8v, v); }
+
+// Four keys' values at one column per lane from rows of the LDS tile (see
+// the kernels for the lanes' addresses).
+__device__ __forceinline__ u2v lds_read_tr(const char *at)
+{
+    return __builtin_bit_cast(
+        u2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4v *)at));
+}
+
+constexpr float kRescale = 8.0f;
+
+// Eight consecutive outputs of a row, d .. d + 7.
+__device__ __forceinline__ void attn_store8(const AttnArgs &p, size_t row, int dim, int d, const float (&f)[8])
+{
+    const size_t at = row * dim + d;
+    if (p.out_kind == OUT_F32) {
+        v4f *o = reinterpret_cast<v4f *>(reinterpret_cast<float *>(p.out) + at);
+        o[0] = v4f{f[0], f[1], f[2], f[3]};
+        o[1] = v4f{f[4], f[5], f[6], f[7]};
+    } else {
+        u4v *o = reinterpret_cast<u4v *>(reinterpret_cast<uint16_t *>(p.out) + at);
+        if (p.out_kind == OUT_BF16)
+            *o = u4v{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+        else
+            *o = u4v{pack_f16(f[0], f[1]), pack_f16(f[2], f[3]), pack_f16(f[4], f[5]), pack_f16(f[6], f[7])};
+    }
+}
+
+// Bytes of the workspace slot of a part of a tile of `rows` rows (a multiple
+// of 128 bytes; sums of 256 threads' runs of eight).
+constexpr int attn_slot_bytes(int rows, int dim)
+{
+    return cdiv_c(rows * dim / 8, 256) * 256 * 32 + cdiv_c(rows * 8, 128) * 128;
+}
+
+// The end of a row tile.  Its NR x D sums lie with the threads of the
+// workgroup as runs of eight columns: run u of thread `tid` is columns
+// 8 (i % (D / 8)) .. + 7 of row i / (D / 8), i = tid + u * NTHR (below the
+// number of runs).  get(u, f, m, l): the run's sums, the row's reference and
+// sum of p.  Writes outputs and lse, or for a split row tile the part,
+// and the whole in the workgroup that arrives last.
+template <int D, int NR, int NTHR, class Get>
+__device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &it, int tid, Get &&get)
+{
+    constexpr int RUNS = D / 8, NU = cdiv_c(NR * RUNS, NTHR);
+    constexpr bool EVEN = NR * RUNS % NTHR == 0;
+    auto mine_is = [&](int u) { return EVEN || tid + u * NTHR < NR * RUNS; };
+    auto write = [&](int u, float (&f)[8], float m, float l) {
+        const int i = tid + u * NTHR, run = i % RUNS;
+        const AttnRow r = attn_row(p, it, it.row0 + i / RUNS);
+        if (r.token < 0)
+            return;
+        const size_t row = (size_t)(it.tok0 + r.token) * (p.heads * p.group) + it.head * p.group + r.head;
+        // (a row that sees no key has l = 0 and sums 0; a NaN is not 0)
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] *= inv;
+        attn_store8(p, row, D, 8 * run, f);
+        if (p.lse && run == 0)
+            p.lse[row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    };
+    if (it.parts == 1) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            if (!mine_is(u))
+                continue;
+            float f[8], m, l;
+            get(u, f, m, l);
+            write(u, f, m, l);
+        }
+        return;
+    }
+    // slot: [NU][2][NTHR] four sums, then [NR] (m, l)
+    constexpr int SUMS = NU * NTHR * 32, SLOT = attn_slot_bytes(NR, D), DEV = 16;
+    static_assert(SLOT >= SUMS + NR * 8, "slot");
+    __shared__ unsigned arrived;
+    const __amdgpu_buffer_rsrc_t mine =
+        make_rsrc(p.parts + (size_t)(it.slot + it.part * it.slot_step) * SLOT, (unsigned)SLOT);
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+        if (!mine_is(u))
+            continue;
+        float f[8], m, l;
+        get(u, f, m, l);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v4f{f[0], f[1], f[2], f[3]}), mine,
+                                               (unsigned)(((2 * u) * NTHR + tid) * 16), 0, DEV);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v4f{f[4], f[5], f[6], f[7]}), mine,
+                                               (unsigned)(((2 * u + 1) * NTHR + tid) * 16), 0, DEV);
+        const int i = tid + u * NTHR;
+        if (i % RUNS == 0)
+            __builtin_amdgcn_raw_buffer_store_b64(u2v{__float_as_uint(m), __float_as_uint(l)}, mine,
+                                                  (unsigned)(SUMS + i / RUNS * 8), 0, DEV);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0)
+        arrived = __hip_atomic_fetch_add(p.counters + it.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (arrived != (unsigned)(it.parts - 1))
+        return;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+        if (!mine_is(u))
+            continue;
+        const int row = (tid + u * NTHR) / RUNS;
+        float f[8] = {0, 0, 0, 0, 0, 0, 0, 0}, m = -__builtin_inff(), l = 0.0f;
+        constexpr int PF = 4;       // parts in flight
+        for (int q0 = 0; q0 < it.parts; q0 += PF) {
+            u4v a[PF], b[PF];
+            u2v ml[PF];
+#pragma unroll
+            for (int q = 0; q < PF; ++q) {
+                const int part = min(q0 + q, it.parts - 1);
+                const __amdgpu_buffer_rsrc_t src =
+                    make_rsrc(p.parts + (size_t)(it.slot + part * it.slot_step) * SLOT, (unsigned)SLOT);
+                ml[q] = __builtin_amdgcn_raw_buffer_load_b64(src, (unsigned)(SUMS + row * 8), 0, DEV);
+                a[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(((2 * u) * NTHR + tid) * 16), 0, DEV);
+                b[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(((2 * u + 1) * NTHR + tid) * 16), 0, DEV);
+            }
+#pragma unroll
+            for (int q = 0; q < PF; ++q) {
+                if (q0 + q >= it.parts)
+                    break;
+                const float mq = __uint_as_float(ml[q][0]), lq = __uint_as_float(ml[q][1]);
+                const float mn = fmaxf(m, mq);
+                // (a part whose keys the row does not see has m = -inf and no sums)
+                const float wa = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+                const float wb = mq == mn ? 1.0f : __builtin_amdgcn_exp2f(mq - mn);
+                const v4f fa = __builtin_bit_cast(v4f, a[q]), fb = __builtin_bit_cast(v4f, b[q]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[e] = f[e] * wa + fa[e] * wb;
+                    f[4 + e] = f[4 + e] * wa + fb[e] * wb;
+                }
+                l = l * wa + lq * wb;
+                m = mn;
+            }
+        }
+        write(u, f, m, l);
+    }
+    if (tid == 0)
+        __hip_atomic_store(p.counters + it.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// ------------------------------------------------------------ few rows
+// Row tiles of 16 QT rows.  The four waves of a workgroup take turns at tiles
+// of 32 keys, each with its own sums, its own LDS and no barrier in the loop;
+// the sums are joined at the end.  Bound: HBM, the cache's bytes; the next
+// tile's codes are in flight while one is worked on.
+//
+// v_mfma_f32_16x16x32_bf16, lane (r = l & 15, g = l >> 4): operands row r,
+// k = 8g .. 8g + 7; accumulator column r, rows 4g .. 4g + 3.  So S^T tile kt
+// (keys 16 kt ..) leaves lane (r, g) with keys 16 kt + 4g + i of query row r,
+// and P^T's eight k of lane group g are keys 4g + i and 16 + 4g + i.
+//
+// LDS of a wave: the keys' tile as operand fragments (lane order, 1 KB each,
+// so the reads are contiguous), then, in the same place, the values' tile
+// as rows of 2D + 32 bytes (the 32 spread the four keys and four lane groups
+// of a transposing read over the banks).
+template <int F, int D, int QT>
+__global__ __launch_bounds__(256)
+void mx_attn_rows(AttnArgs p)
+{
+    constexpr int KT = 32, BM = 16 * QT, BN = 4 * KT;
+    using G = AttnGeom<F, D, KT, 64>;
+    constexpr int KS = D / 32, DT = D / 16, NP = G::VC / 8;
+    constexpr int KBYTES = 2 * KS * 1024, VROW = 2 * D + 32, VBYTES = KT * VROW;
+    constexpr int WBYTES = KBYTES > VBYTES ? KBYTES : VBYTES;
+    constexpr int OROW = D + 4;                         // floats of a row of sums in LDS
+    constexpr int OBYTES = 16 * OROW * 4;               // one wave's 16 rows
+    constexpr int BYTES = (WBYTES > OBYTES ? WBYTES : OBYTES) * 4;
+    __shared__ __attribute__((aligned(1024))) char lds[BYTES];
+    __shared__ float ml[4][BM][2];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g = lane >> 4;
+
+    AttnItem it;
+    if (!plan_item<BM, BN>(p, 1, it))
+        return;
+
+    AttnRow row[QT];
+    bf16x8v q[QT][KS];
+    int lo_most = 0, hi_least = 0x7FFFFFFF;             // keys that every row of the tile sees
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        row[t] = attn_row(p, it, it.row0 + 16 * t + r);
+        const uint16_t *src = p.q + (long long)(it.tok0 + max(row[t].token, 0)) * p.q_stride +
+                              (long long)(it.head * p.group + row[t].head) * D + 8 * g;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            q[t][s] = as_bf16x8(row[t].token >= 0 ? *reinterpret_cast<const u4v *>(src + 32 * s) : u4v{0u, 0u, 0u, 0u});
+        if (row[t].token >= 0) {
+            lo_most = max(lo_most, row[t].lo);
+            hi_least = min(hi_least, row[t].hi);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) {
+        lo_most = max(lo_most, __shfl_xor(lo_most, d));
+        hi_least = min(hi_least, __shfl_xor(hi_least, d));
+    }
+    lo_most = uniform(lo_most);
+    hi_least = uniform(hi_least);
+
+    char *mem = lds + wave * WBYTES;
+    const int *table = p.table + it.seq * p.table_stride;
+    const int mykey = lane / G::CH, chunk = lane % G::CH;
+    v4f o[QT][DT];
+    float m[QT], l[QT];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        m[t] = -__builtin_inff();
+        l[t] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+            o[t][d] = v4f{0, 0, 0, 0};
+    }
+
+    AttnTileRegs<G> cur;
+    int page[G::NL];
+    auto pages_of = [&](int key) {
+#pragma unroll
+        for (int j = 0; j < G::NL; ++j)
+            page[j] = attn_page(p, table, key + mykey + j * G::KPL, it.key1);
+    };
+    int key = it.key0 + wave * KT;
+    if (key < it.key1) {
+        pages_of(key);
+        attn_load<G>(p, it.head, key + mykey, chunk, page, cur);
+        pages_of(key + BN);
+    }
+    auto store_values = [&](int j, const u4v &codes, unsigned scale, bool ok, int mode) {
+        u4v w[NP];
+        attn_expand<F>(codes, scale, w);
+        char *at = mem + (mykey + j * G::KPL) * VROW + chunk * G::VC * 2;
+#pragma unroll
+        for (int e = 0; e < NP; ++e)
+            *reinterpret_cast<u4v *>(at + 16 * e) = values_mode(w[e], ok, mode);
+    };
+    auto wave_fence = [] {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+    const char *vread = mem + (4 * g + (r >> 2)) * VROW + (r & 3) * 8;
+    // values of keys 4g .. and 16 + 4g .., columns 16 d + r
+    auto values_at = [&](int d) {
+        const u2v a = lds_read_tr(vread + 32 * d), b = lds_read_tr(vread + 16 * VROW + 32 * d);
+        return as_bf16x8(u4v{a.x, a.y, b.x, b.y});
+    };
+    for (; key < it.key1; key += BN) {
+        // keys into LDS: chunk (key kk, values VC chunk ..) is pieces of eight
+        // values, each one lane's operand of one 32-deep step
+#pragma unroll
+        for (int j = 0; j < G::NL; ++j) {
+            u4v w[NP];
+            attn_expand<F>(cur.k[j], cur.ks[j], w);
+            const int kk = mykey + j * G::KPL;
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const int piece = chunk * NP + e;       // of the key's D / 8
+                *reinterpret_cast<u4v *>(mem + (((kk >> 4) * KS + (piece >> 2)) * 64 + (piece & 3) * 16 + (kk & 15)) * 16) = w[e];
+            }
+        }
+        wave_fence();
+        v4f x[QT][2];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const bf16x8v f = as_bf16x8(*reinterpret_cast<const u4v *>(mem + ((kt * KS + s) * 64 + lane) * 16));
+#pragma unroll
+                for (int t = 0; t < QT; ++t)
+                    x[t][kt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[t][s], s ? x[t][kt] : v4f{0, 0, 0, 0}, 0, 0, 0);
+            }
+        wave_fence();
+        // values into the same place, and the next tile's codes on their way
+        bool ok = true, nan = false;
+#pragma unroll
+        for (int j = 0; j < G::NL; ++j) {
+            ok &= cur.ok[j];
+            nan |= attn_has_nan<F>(cur.v[j], cur.vs[j]) && cur.ok[j];
+        }
+        const bool whole = __all(ok) && key >= lo_most && key + KT <= hi_least;
+        const bool careful = !whole && __any(nan);
+#pragma unroll
+        for (int j = 0; j < G::NL; ++j)
+            store_values(j, cur.v[j], cur.vs[j], cur.ok[j], careful ? VALUES_CLEAN : VALUES_PLAIN);
+        unsigned vis[QT];                   // bit 4 kt + i: the row sees key 16 kt + 4g + i
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+            vis[t] = 0xFFu;
+        if (!whole) {
+            unsigned here = 0;              // the lane that loaded a key's first chunk knows
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int kk = 16 * (e >> 2) + 4 * g + (e & 3);
+#pragma unroll
+                for (int j = 0; j < G::NL; ++j) {
+                    const int v = __shfl((int)cur.ok[j], (kk % G::KPL) * G::CH);
+                    here |= (unsigned)(kk / G::KPL == j && v) << e;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+                vis[t] = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int k = key + 16 * (e >> 2) + 4 * g + (e & 3);
+                    vis[t] |= (unsigned)(k >= row[t].lo && k < row[t].hi) << e;
+                }
+                vis[t] &= here;
+            }
+        }
+        if (key + BN < it.key1) {
+            attn_load<G>(p, it.head, key + BN + mykey, chunk, page, cur);
+            pages_of(key + 2 * BN);
+        }
+        bf16x8v pb[QT];
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            if (!whole) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[t][e >> 2][e & 3] = (vis[t] >> e & 1) ? x[t][e >> 2][e & 3] : -__builtin_inff();
+            }
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                top = fmaxf(top, x[t][e >> 2][e & 3]);
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32)) * p.c;
+            if (__any(top > m[t] + kRescale)) {
+                const float mn = fmaxf(m[t], top);
+                const float w = m[t] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[t] - mn);
+                l[t] *= w;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[t][d][i] *= w;
+                m[t] = mn;
+            }
+            // (no key seen yet: m = -inf, every x = -inf, p = 0)
+            const float ref = m[t] == -__builtin_inff() ? 0.0f : m[t];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float w = __builtin_amdgcn_exp2f(fmaf(x[t][e >> 2][e & 3], p.c, -ref));
+                l[t] += w;
+                pb[t][e] = (__bf16)w;
+            }
+        }
+        wave_fence();
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            const bf16x8v f = values_at(d);
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+                o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, pb[t], o[t][d], 0, 0, 0);
+        }
+        wave_fence();
+        if (careful) {
+            // ones where the values are NaN; a row that sees one gets a NaN there
+#pragma unroll
+            for (int j = 0; j < G::NL; ++j) {
+                const int k = key + mykey + j * G::KPL, pg = attn_page(p, table, k, it.key1);
+                const long long at = attn_row_at(p, pg, it.head, k);
+                store_values(j, *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + 16 * chunk),
+                             p.scales[1][at * G::SB + chunk * G::VC / 32], pg >= 0, VALUES_NAN);
+            }
+            wave_fence();
+            bf16x8v seen[QT];
+#pragma unroll
+            for (int t = 0; t < QT; ++t)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    seen[t][e] = (vis[t] >> e & 1) ? (__bf16)1.0f : (__bf16)0.0f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const bf16x8v f = values_at(d);
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    const v4f bad = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, seen[t], v4f{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[t][d][i] = bad[i] > 0.0f ? __builtin_nanf("") : o[t][d][i];
+                }
+            }
+            wave_fence();
+        }
+    }
+
+    // join the four waves, 16 rows at a time
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        l[t] += __shfl_xor(l[t], 16);
+        l[t] += __shfl_xor(l[t], 32);
+        if (g == 0) {
+            ml[wave][16 * t + r][0] = m[t];
+            ml[wave][16 * t + r][1] = l[t];
+        }
+    }
+    __syncthreads();
+    // (run i of the 16 QT rows' runs of eight columns: thread i % 256)
+    constexpr int RUNS = D / 8, NU = cdiv_c(BM * RUNS, 256);
+    float f[NU][8], fm[NU], fl[NU];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            top = fmaxf(top, ml[w][16 * t + r][0]);
+        const float w = m[t] == top ? 1.0f : __builtin_amdgcn_exp2f(m[t] - top);
+        float *mine = reinterpret_cast<float *>(lds) + wave * (OBYTES / 4) + r * OROW + 4 * g;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            v4f s = o[t][d];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[i] *= w;
+            *reinterpret_cast<v4f *>(mine + 16 * d) = s;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            if (256 * (u + 1) <= t * 16 * RUNS || 256 * u >= (t + 1) * 16 * RUNS)
+                continue;
+            const int i = tid + 256 * u, n = i / RUNS, col = i % RUNS * 8;
+            if (n >> 4 != t)
+                continue;
+            fm[u] = -__builtin_inff();
+            fl[u] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[u][e] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                fm[u] = fmaxf(fm[u], ml[v][n][0]);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const float mv = ml[v][n][0];
+                fl[u] += ml[v][n][1] * (mv == fm[u] ? 1.0f : __builtin_amdgcn_exp2f(mv - fm[u]));
+                const float *src = reinterpret_cast<const float *>(lds) + v * (OBYTES / 4) + (n & 15) * OROW + col;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[u][e] += src[e];
+            }
+        }
+        __syncthreads();
+    }
+    attn_finish<D, BM, 256>(p, it, tid, [&](int u, float (&out)[8], float &mm, float &ll) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            out[e] = f[u][e];
+        mm = fm[u];
+        ll = fl[u];
+    });
+}
+
+// ------------------------------------------------------------ many rows
+// Row tiles of 128 rows, 32 per wave, over tiles of 64 keys that the four
+// waves expand together into one of two LDS buffers: while tile t is worked
+// on, tile t+1's codes, loaded during tile t-1, are expanded into the other
+// buffer and tile t+2's loads are issued; one barrier per tile.  Bound: MFMA
+// and, next to it, the softmax's VALU work.
+//
+// v_mfma_f32_32x32x16_bf16, lane (r = l & 31, h = l >> 5): operands row r,
+// k = 8h .. 8h + 7; accumulator column r, register i row 8 (i >> 2) + 4h +
+// (i & 3).  So P^T's eight k of step s and half h are keys 16s + 4h + i and
+// 16s + 8 + 4h + i of the tile.
+//
+// LDS of a buffer: the keys as operand fragments (lane order, 1 KB each,
+// apart by 1 KB + 128 bytes so that the expanding stores of a key's steps
+// fall on different banks), then the values as rows of 2D + 64 bytes (the
+// four keys and two column groups of a half's transposing read then cover
+// the banks once).
+template <int F, int D>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void mx_attn_tile(AttnArgs p)
+{
+    constexpr int BM = 128, BN = 64;
+    using G = AttnGeom<F, D, BN, 256>;
+    constexpr int KS = D / 16, DT = D / 32, NP = G::VC / 8;
+    constexpr int FS = 1024 + 128, KBYTES = 2 * KS * FS, VROW = 2 * D + 64, VBYTES = BN * VROW;
+    constexpr int BUF = KBYTES + VBYTES;
+    constexpr int OROW = D + 4;
+    constexpr int BYTES = 2 * BUF > BM * OROW * 4 ? 2 * BUF : BM * OROW * 4;
+    __shared__ __attribute__((aligned(1024))) char lds[BYTES];
+    __shared__ float ml[BM][2];
+    __shared__ unsigned flags[2][4];                    // of each wave's keys: 1 not all there, 2 a NaN among the values
+    __shared__ unsigned char there[2][BN];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 31, h = lane >> 5;
+
+    AttnItem it;
+    if (!plan_item<BM, BN>(p, 4, it))
+        return;
+
+    const AttnRow row = attn_row(p, it, it.row0 + 32 * wave + r);
+    bf16x8v q[KS];
+    {
+        const uint16_t *src = p.q + (long long)(it.tok0 + max(row.token, 0)) * p.q_stride +
+                              (long long)(it.head * p.group + row.head) * D + 8 * h;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            q[s] = as_bf16x8(row.token >= 0 ? *reinterpret_cast<const u4v *>(src + 16 * s) : u4v{0u, 0u, 0u, 0u});
+    }
+    // keys that every row of the wave sees, and keys that some row may see
+    int lo_most = row.token >= 0 ? row.lo : 0, hi_least = row.token >= 0 ? row.hi : 0x7FFFFFFF;
+    int lo_least = row.token >= 0 ? row.lo : 0x7FFFFFFF, hi_most = row.hi;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        lo_most = max(lo_most, __shfl_xor(lo_most, d));
+        hi_least = min(hi_least, __shfl_xor(hi_least, d));
+        lo_least = min(lo_least, __shfl_xor(lo_least, d));
+        hi_most = max(hi_most, __shfl_xor(hi_most, d));
+    }
+    lo_most = uniform(lo_most);
+    hi_least = uniform(hi_least);
+    lo_least = uniform(lo_least);
+    hi_most = uniform(hi_most);
+
+    const int *table = p.table + it.seq * p.table_stride;
+    const bool loads = G::ALL || tid < G::KPL * G::CH;
+    const int mykey = tid / G::CH, chunk = tid % G::CH;
+    v16f o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            o[d][i] = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f;
+
+    AttnTileRegs<G> cur;
+    int page[G::NL];
+    auto pages_of = [&](int key) {
+#pragma unroll
+        for (int j = 0; j < G::NL; ++j)
+            page[j] = loads ? attn_page(p, table, key + mykey + j * G::KPL, it.key1) : -1;
+    };
+    auto load = [&](int key) { attn_load<G>(p, it.head, key + mykey, chunk, page, cur); };
+    auto store_values = [&](char *buf, int j, const u4v &codes, unsigned scale, bool ok, int mode) {
+        u4v w[NP];
+        attn_expand<F>(codes, scale, w);
+        char *at = buf + KBYTES + (mykey + j * G::KPL) * VROW + chunk * G::VC * 2;
+#pragma unroll
+        for (int e = 0; e < NP; ++e)
+            *reinterpret_cast<u4v *>(at + 16 * e) = values_mode(w[e], ok, mode);
+    };
+    // the loaded tile into buffer b
+    auto expand = [&](int b) {
+        char *buf = lds + b * BUF;
+        bool gone = false, nan = false;
+        if (loads) {
+#pragma unroll
+            for (int j = 0; j < G::NL; ++j) {
+                const int kk = mykey + j * G::KPL;
+                gone |= !cur.ok[j];
+                nan |= attn_has_nan<F>(cur.v[j], cur.vs[j]) && cur.ok[j];
+                u4v w[NP];
+                attn_expand<F>(cur.k[j], cur.ks[j], w);
+#pragma unroll
+                for (int e = 0; e < NP; ++e) {
+                    const int piece = chunk * NP + e;
+                    *reinterpret_cast<u4v *>(buf + ((kk >> 5) * KS + (piece >> 1)) * FS + (piece & 1) * 512 + (kk & 31) * 16) = w[e];
+                }
+                store_values(buf, j, cur.v[j], cur.vs[j], cur.ok[j], VALUES_PLAIN);
+                if (chunk == 0)
+                    there[b][kk] = cur.ok[j];
+            }
+        }
+        const unsigned fl = (__any(gone) ? 1u : 0u) | (__any(nan) ? 2u : 0u);
+        if (lane == 0)
+            flags[b][wave] = fl;
+    };
+    const int vread = (4 * h + ((r & 15) >> 2)) * VROW + 32 * (r >> 4) + 8 * (r & 3);
+    // values of keys 16 s + 4h .. and 16 s + 8 + 4h .., columns 32 d + r
+    auto values_at = [&](const char *buf, int d, int s) {
+        const char *at = buf + KBYTES + vread + 16 * s * VROW + 64 * d;
+        const u2v a = lds_read_tr(at), b = lds_read_tr(at + 8 * VROW);
+        return as_bf16x8(u4v{a.x, a.y, b.x, b.y});
+    };
+
+    int key = it.key0;
+    if (key < it.key1) {
+        pages_of(key);
+        load(key);
+        pages_of(key + BN);
+        expand(0);
+        if (key + BN < it.key1) {
+            load(key + BN);
+            pages_of(key + 2 * BN);
+        }
+    }
+    block_barrier();
+    for (int b = 0; key < it.key1; key += BN, b ^= 1) {
+        if (key + BN < it.key1) {
+            expand(b ^ 1);
+            if (key + 2 * BN < it.key1) {
+                load(key + 2 * BN);
+                pages_of(key + 3 * BN);
+            }
+        }
+        char *buf = lds + b * BUF;
+        const unsigned fl = flags[b][0] | flags[b][1] | flags[b][2] | flags[b][3];
+        // (uniform over the workgroup: the values are rewritten below)
+        const bool careful = (uniform(fl) & 2) && !(key >= it.all_lo && key + BN <= it.all_hi && !(uniform(fl) & 1));
+        if (careful) {
+#pragma unroll
+            for (int j = 0; j < G::NL; ++j)
+                if (loads) {
+                    const int k = key + mykey + j * G::KPL, pg = attn_page(p, table, k, it.key1);
+                    const long long at = attn_row_at(p, pg, it.head, k);
+                    store_values(buf, j, *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + 16 * chunk),
+                                 p.scales[1][at * G::SB + chunk * G::VC / 32], pg >= 0, VALUES_CLEAN);
+                }
+            block_barrier();
+        }
+        unsigned vis = 0xFFFFFFFFu;         // bit 16 kt + i: the row sees key 32 kt + 8 (i >> 2) + 4h + (i & 3)
+        if (key < hi_most && key + BN > lo_least) {
+            v16f x[2];
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt) {
+                    const bf16x8v f = as_bf16x8(*reinterpret_cast<const u4v *>(buf + (kt * KS + s) * FS + lane * 16));
+                    if (s == 0)
+                        x[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[s], v16f{}, 0, 0, 0);
+                    else
+                        x[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[s], x[kt], 0, 0, 0);
+                }
+            if (!(key >= lo_most && key + BN <= hi_least && !(uniform(fl) & 1))) {
+                vis = 0;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int kk = 32 * (e >> 4) + 8 * ((e & 15) >> 2) + 4 * h + (e & 3), k = key + kk;
+                    const bool see = k >= row.lo && k < row.hi && there[b][kk];
+                    vis |= (unsigned)see << e;
+                    x[e >> 4][e & 15] = see ? x[e >> 4][e & 15] : -__builtin_inff();
+                }
+            }
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                top = fmaxf(top, x[e >> 4][e & 15]);
+            top = fmaxf(top, __shfl_xor(top, 32)) * p.c;
+            if (__any(top > m + kRescale)) {
+                const float mn = fmaxf(m, top);
+                const float w = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+                l *= w;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[d][i] *= w;
+                m = mn;
+            }
+            const float ref = m == -__builtin_inff() ? 0.0f : m;
+            bf16x8v pb[4];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const float w = __builtin_amdgcn_exp2f(fmaf(x[e >> 4][e & 15], p.c, -ref));
+                l += w;
+                pb[e >> 3][e & 7] = (__bf16)w;
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_at(buf, d, s), pb[s], o[d], 0, 0, 0);
+        } else {
+            vis = 0;
+        }
+        if (careful) {
+            // ones where the values are NaN; a row that sees one gets a NaN there
+            block_barrier();
+#pragma unroll
+            for (int j = 0; j < G::NL; ++j)
+                if (loads) {
+                    const int k = key + mykey + j * G::KPL, pg = attn_page(p, table, k, it.key1);
+                    const long long at = attn_row_at(p, pg, it.head, k);
+                    store_values(buf, j, *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + 16 * chunk),
+                                 p.scales[1][at * G::SB + chunk * G::VC / 32], pg >= 0, VALUES_NAN);
+                }
+            block_barrier();
+            bf16x8v seen[4];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                seen[e >> 3][e & 7] = (vis >> e & 1) ? (__bf16)1.0f : (__bf16)0.0f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                v16f bad = {};
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    bad = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_at(buf, d, s), seen[s], bad, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[d][i] = bad[i] > 0.0f ? __builtin_nanf("") : o[d][i];
+            }
+        }
+        block_barrier();
+    }
+
+    l += __shfl_xor(l, 32);
+    if (h == 0) {
+        ml[32 * wave + r][0] = m;
+        ml[32 * wave + r][1] = l;
+    }
+    float *mine = reinterpret_cast<float *>(lds) + (32 * wave + r) * OROW + 4 * h;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<v4f *>(mine + 32 * d + 8 * i) = v4f{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+    __syncthreads();
+    attn_finish<D, BM, 256>(p, it, tid, [&](int u, float (&f)[8], float &mm, float &ll) {
+        constexpr int RUNS = D / 8;
+        const int i = tid + 256 * u, n = i / RUNS;
+        const float *src = reinterpret_cast<const float *>(lds) + n * OROW + i % RUNS * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = src[e];
+        mm = ml[n][0];
+        ll = ml[n][1];
+    });
+}
+
+}  // namespace mxg

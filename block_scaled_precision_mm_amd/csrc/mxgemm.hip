@@ -20,6 +20,7 @@
 #include "../../include/mxgemm.h"
 #include "mx_decode.hpp"
 #include "mx_dense.hpp"
+#include "mx_host.hpp"
 #include "mx_quant.hpp"
 #include "mx_stream.hpp"
 #include "mx_tile.hpp"
@@ -960,6 +961,20 @@ int run_default(int is_fp4, const void *a, const void *b, const void *sa, const 
 }
 
 }  // namespace
+
+namespace mxg {
+
+int host_check_device() { return check_device(); }
+
+int host_hip_status(hipError_t e)
+{
+    if (e == hipSuccess)
+        return MXG_OK;
+    g_last_hip_error = (int)e;
+    return MXG_ERR_HIP;
+}
+
+}  // namespace mxg
 
 extern "C" {
 

@@ -1,0 +1,358 @@
+// mxserve.hip -- host side of the operators around the products: RMSNorm into
+// the next product's A operand, the paged key/value cache in MX formats and
+// the attention over it.  Argument validation, configuration choice and
+// launches behind the C ABI declared in include/mxgemm.h.
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "../../include/mxgemm.h"
+#include "mx_attn.hpp"
+#include "mx_host.hpp"
+#include "mx_norm.hpp"
+
+using namespace mxg;
+
+namespace {
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+FastDiv fast_div(unsigned d)
+{
+    FastDiv f = {d, 0, 0};
+    if (d > 1) {
+        while ((2ull << f.s) < d)
+            ++f.s;
+        f.m = (unsigned)(((1ull << (32 + f.s)) + d - 1) / d);
+    }
+    return f;
+}
+
+// ------------------------------------------------------------------- RMSNorm
+// Longest row: 1024 threads hold 64 values each.
+constexpr int64_t kMaxNormK = 65536;
+
+template <int THR, int NV>
+int launch_norm(const NormArgs &a, int64_t rows, int out_kind, hipStream_t stream)
+{
+    void (*fn)(NormArgs) = nullptr;
+    switch (out_kind) {
+    case MXG_OUT_BF16: fn = &mx_rmsnorm_rows<THR, NV, OUT_BF16>; break;
+    case MXG_OUT_F16: fn = &mx_rmsnorm_rows<THR, NV, OUT_F16>; break;
+    case MXG_OUT_F32: fn = &mx_rmsnorm_rows<THR, NV, OUT_F32>; break;
+    case MXG_OUT_MXFP8: fn = &mx_rmsnorm_rows<THR, NV, OUT_MX8>; break;
+    default: fn = &mx_rmsnorm_rows<THR, NV, OUT_MX4>; break;
+    }
+    hipLaunchKernelGGL(fn, dim3((unsigned)rows), dim3(THR), 0, stream, a);
+    return host_hip_status(hipGetLastError());
+}
+
+int run_norm(const void *x, const void *residual, const void *weight, void *h, void *y, void *y_scale,
+             int64_t rows, int64_t K, float eps, int out_kind, hipStream_t stream)
+{
+    if (rows != 0 && (!x || !y))
+        return MXG_ERR_NULL;
+    if (out_kind < MXG_OUT_BF16 || out_kind > MXG_OUT_MXFP4)
+        return MXG_ERR_DTYPE;
+    const bool mx = out_kind == MXG_OUT_MXFP8 || out_kind == MXG_OUT_MXFP4;
+    if (rows != 0 && mx && !y_scale)
+        return MXG_ERR_NULL;
+    if (rows < 0 || rows > INT32_MAX || K < 1 || K > kMaxNormK)
+        return MXG_ERR_SHAPE;
+    if (K % 32)
+        return MXG_ERR_K_ALIGN;
+    if (!(eps >= 0.0f) || !isfinite(eps))
+        return MXG_ERR_CONFIG;
+    if (((uintptr_t)x | (uintptr_t)residual | (uintptr_t)weight | (uintptr_t)h | (uintptr_t)y) & 15)
+        return MXG_ERR_PTR_ALIGN;
+    int rc = host_check_device();
+    if (rc || rows == 0)
+        return rc;
+    const NormArgs a = {(const uint16_t *)x, (const uint16_t *)residual, (const uint16_t *)weight,
+                        (uint16_t *)h, y, (uint8_t *)y_scale, (int)K, eps};
+    // one workgroup per row: a wave up to 512 values, 256 threads up to 16384
+    // (at most eight 16-byte pieces each), 1024 beyond
+    const int64_t pieces = K / 8;
+    if (pieces <= 64)
+        return launch_norm<64, 1>(a, rows, out_kind, stream);
+    switch (cdiv(pieces, 256)) {
+    case 1: return launch_norm<256, 1>(a, rows, out_kind, stream);
+    case 2: return launch_norm<256, 2>(a, rows, out_kind, stream);
+    case 3: return launch_norm<256, 3>(a, rows, out_kind, stream);
+    case 4: return launch_norm<256, 4>(a, rows, out_kind, stream);
+    case 5: case 6: return launch_norm<256, 6>(a, rows, out_kind, stream);
+    case 7: case 8: return launch_norm<256, 8>(a, rows, out_kind, stream);
+    }
+    return pieces <= 4096 ? launch_norm<1024, 4>(a, rows, out_kind, stream)
+                          : launch_norm<1024, 8>(a, rows, out_kind, stream);
+}
+
+// --------------------------------------------------------------------- cache
+int log2_of(int64_t v)
+{
+    int s = 0;
+    while (((int64_t)1 << s) < v)
+        ++s;
+    return s;
+}
+
+constexpr int64_t kMaxPage = 65536, kMaxHeads = 4096, kMaxHeadDim = 1024;
+
+int validate_cache(const mxg_kv_cache_t *c)
+{
+    if (!c || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales)
+        return MXG_ERR_NULL;
+    if (c->pages < 1 || c->pages > INT32_MAX || c->page_size < 1 || c->page_size > kMaxPage ||
+        (c->page_size & (c->page_size - 1)) || c->kv_heads < 1 || c->kv_heads > kMaxHeads ||
+        c->head_dim < 1 || c->head_dim > kMaxHeadDim)
+        return MXG_ERR_SHAPE;
+    if (c->head_dim % 32)
+        return MXG_ERR_K_ALIGN;
+    // (codes and element offsets within 2^62: far past any memory)
+    if (c->pages * c->page_size > ((int64_t)1 << 40))
+        return MXG_ERR_SHAPE;
+    if (((uintptr_t)c->k_codes | (uintptr_t)c->v_codes) & 15)
+        return MXG_ERR_PTR_ALIGN;
+    if (((uintptr_t)c->k_scales | (uintptr_t)c->v_scales) & 3)
+        return MXG_ERR_PTR_ALIGN;
+    return MXG_OK;
+}
+
+int run_cache(bool write, const mxg_kv_cache_t *c, const void *k, const void *v, int64_t k_stride,
+              int64_t v_stride, const int64_t *slots, int64_t tokens, hipStream_t stream)
+{
+    int rc = validate_cache(c);
+    if (rc)
+        return rc;
+    if (tokens < 0)
+        return MXG_ERR_SHAPE;
+    if (tokens > 0 && (!k || !v || !slots))
+        return MXG_ERR_NULL;
+    const int64_t width = c->kv_heads * c->head_dim;
+    if (tokens > ((int64_t)1 << 30) / (width / 8) || k_stride < width || v_stride < width ||
+        k_stride > INT32_MAX || v_stride > INT32_MAX)
+        return MXG_ERR_SHAPE;
+    if ((k_stride | v_stride) % 8)
+        return MXG_ERR_K_ALIGN;
+    if (((uintptr_t)k | (uintptr_t)v) & 15 || ((uintptr_t)slots & 7))
+        return MXG_ERR_PTR_ALIGN;
+    rc = host_check_device();
+    if (rc || tokens == 0)
+        return rc;
+    CacheArgs a;
+    a.codes[0] = (uint8_t *)c->k_codes;
+    a.codes[1] = (uint8_t *)c->v_codes;
+    a.scales[0] = (uint8_t *)c->k_scales;
+    a.scales[1] = (uint8_t *)c->v_scales;
+    a.in[0] = (const uint16_t *)k;
+    a.in[1] = (const uint16_t *)v;
+    a.out[0] = (uint16_t *)k;
+    a.out[1] = (uint16_t *)v;
+    a.stride[0] = k_stride;
+    a.stride[1] = v_stride;
+    a.slots = (const long long *)slots;
+    a.nslots = c->pages * c->page_size;
+    a.n = (int)(tokens * (width / 8));
+    a.heads = (int)c->kv_heads;
+    a.dim = (int)c->head_dim;
+    a.page_shift = log2_of(c->page_size);
+    a.per_token = fast_div((unsigned)(width / 8));
+    a.per_head = fast_div((unsigned)(c->head_dim / 8));
+    void (*fn)(CacheArgs) = write ? (c->is_fp4 ? &mx_cache_write<FMT_FP4> : &mx_cache_write<FMT_FP8>)
+                                  : (c->is_fp4 ? &mx_cache_read<FMT_FP4> : &mx_cache_read<FMT_FP8>);
+    hipLaunchKernelGGL(fn, dim3((unsigned)cdiv(a.n, 512), 2), dim3(256), 0, stream, a);
+    return host_hip_status(hipGetLastError());
+}
+
+// ----------------------------------------------------------------- attention
+typedef void (*AttnFn)(AttnArgs);
+
+// One kernel of the launch: rows per tile, workgroups that can run at once.
+struct AttnKernel {
+    AttnFn fn;
+    int bm, target;
+};
+
+// Row tiles of 16 (32) rows in mx_attn_rows, of 128 in mx_attn_tile.
+enum { ROWS_16 = 0, ROWS_32 = 1, ROWS_128 = 2 };
+constexpr int kAttnBM[3] = {16, 32, 128};
+
+template <int F, int D>
+AttnFn attn_fn(int which)
+{
+    return which == ROWS_16 ? &mx_attn_rows<F, D, 1> : which == ROWS_32 ? &mx_attn_rows<F, D, 2> : &mx_attn_tile<F, D>;
+}
+
+AttnKernel attn_kernel(int which, bool fp4, int dim)
+{
+    AttnKernel k;
+    k.bm = kAttnBM[which];
+    k.target = which == ROWS_16 ? 1024 : 512;
+    if (dim == 64)
+        k.fn = fp4 ? attn_fn<FMT_FP4, 64>(which) : attn_fn<FMT_FP8, 64>(which);
+    else
+        k.fn = fp4 ? attn_fn<FMT_FP4, 128>(which) : attn_fn<FMT_FP8, 128>(which);
+    return k;
+}
+
+// What a call launches: one kernel for all sequences, or one for those of
+// few rows (new tokens x heads of a group) and one for the others.
+struct AttnPlan {
+    int n;
+    int which[2];
+    int above[2], upto[2];
+    int64_t base[2];        // most row tiles
+    size_t bytes[2];        // of the workspace for splitting; 0: none
+};
+
+AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, int64_t dim, int64_t max_new)
+{
+    AttnPlan p = {};
+    const int64_t most = max_new * group;       // rows of the longest
+    if (most <= 16 || most <= 32 || tokens == seqs * max_new) {
+        p.n = 1;
+        p.which[0] = most <= 16 ? ROWS_16 : most <= 32 ? ROWS_32 : ROWS_128;
+        p.above[0] = 0;
+        p.upto[0] = INT32_MAX;
+    } else {
+        p.n = 2;
+        p.which[0] = ROWS_128;
+        p.above[0] = 32;
+        p.upto[0] = INT32_MAX;
+        p.which[1] = ROWS_32;
+        p.above[1] = 0;
+        p.upto[1] = 32;
+    }
+    for (int i = 0; i < p.n; ++i) {
+        const int bm = kAttnBM[p.which[i]];
+        const AttnKernel k = attn_kernel(p.which[i], false, (int)dim);
+        const int64_t some = std::min(seqs, tokens);        // sequences with a new token
+        p.base[i] = heads * (p.upto[i] <= bm ? some : tokens * group / bm + some);
+        p.bytes[i] = p.base[i] <= kSplitCounters ? (size_t)2 * k.target * attn_slot_bytes(bm, (int)dim) : 0;
+    }
+    return p;
+}
+
+bool attn_shape_ok(const mxg_kv_cache_t *c, int64_t seqs, int64_t tokens, int64_t q_heads, int64_t max_new)
+{
+    return seqs >= 0 && seqs <= 65536 && tokens >= 0 && q_heads >= c->kv_heads && q_heads <= 65536 &&
+           q_heads % c->kv_heads == 0 && tokens <= ((int64_t)1 << 30) / q_heads && max_new >= 0 &&
+           max_new <= INT32_MAX && (c->head_dim == 64 || c->head_dim == 128);
+}
+
+size_t attn_workspace(const AttnPlan &p)
+{
+    size_t most = 0;
+    for (int i = 0; i < p.n; ++i)
+        most = std::max(most, p.bytes[i]);
+    return most ? most + kSplitCounters * sizeof(unsigned) : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mx_rmsnorm(const void *x, const void *residual, const void *weight, void *h, void *y, void *y_scale,
+               int64_t rows, int64_t K, float eps, int out_kind, mxg_stream_t stream)
+{
+    return run_norm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind, (hipStream_t)stream);
+}
+
+int mx_kv_cache_write(const mxg_kv_cache_t *cache, const void *k, const void *v, int64_t k_stride,
+                      int64_t v_stride, const int64_t *slots, int64_t tokens, mxg_stream_t stream)
+{
+    return run_cache(true, cache, k, v, k_stride, v_stride, slots, tokens, (hipStream_t)stream);
+}
+
+int mx_kv_cache_read(const mxg_kv_cache_t *cache, void *k, void *v, int64_t k_stride, int64_t v_stride,
+                     const int64_t *slots, int64_t tokens, mxg_stream_t stream)
+{
+    return run_cache(false, cache, k, v, k_stride, v_stride, slots, tokens, (hipStream_t)stream);
+}
+
+size_t mx_paged_attention_workspace_bytes(const mxg_kv_cache_t *cache, int64_t seqs, int64_t tokens,
+                                          int64_t q_heads, int64_t max_new)
+{
+    if (validate_cache(cache) || !attn_shape_ok(cache, seqs, tokens, q_heads, max_new))
+        return 0;
+    return attn_workspace(attn_plan(seqs, tokens, cache->kv_heads, q_heads / cache->kv_heads, cache->head_dim, max_new));
+}
+
+int mx_paged_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, const int32_t *ends,
+                       const int32_t *lens, const int32_t *table, int64_t table_width, int64_t seqs,
+                       int64_t tokens, int64_t q_heads, int64_t max_new, float scale, int causal,
+                       int64_t window, void *out, int out_dtype, float *lse, void *workspace,
+                       size_t workspace_bytes, mxg_stream_t stream)
+{
+    int rc = validate_cache(cache);
+    if (rc)
+        return rc;
+    if (out_dtype < MXG_OUT_BF16 || out_dtype > MXG_OUT_F32)
+        return MXG_ERR_DTYPE;
+    if (!attn_shape_ok(cache, seqs, tokens, q_heads, max_new) || table_width < 0 ||
+        table_width > ((int64_t)1 << 30) / cache->page_size || q_stride < q_heads * cache->head_dim ||
+        q_stride > INT32_MAX || window < 0)
+        return MXG_ERR_SHAPE;
+    if (tokens > 0 && seqs > 0 && (!q || !ends || !lens || !out || (table_width > 0 && !table)))
+        return MXG_ERR_NULL;
+    if (q_stride % 8)
+        return MXG_ERR_K_ALIGN;
+    if (!(scale > 0.0f) || !isfinite(scale) || (causal != 0 && causal != 1))
+        return MXG_ERR_CONFIG;
+    if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15)
+        return MXG_ERR_PTR_ALIGN;
+    if (((uintptr_t)ends | (uintptr_t)lens | (uintptr_t)table | (uintptr_t)lse) & 3)
+        return MXG_ERR_PTR_ALIGN;
+    rc = host_check_device();
+    if (rc || tokens == 0 || seqs == 0)
+        return rc;
+    const int64_t group = q_heads / cache->kv_heads;
+    const AttnPlan plan = attn_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new);
+    const bool split = workspace && workspace_bytes >= attn_workspace(plan);
+    AttnArgs a;
+    a.codes[0] = (const uint8_t *)cache->k_codes;
+    a.codes[1] = (const uint8_t *)cache->v_codes;
+    a.scales[0] = (const uint8_t *)cache->k_scales;
+    a.scales[1] = (const uint8_t *)cache->v_scales;
+    a.q = (const uint16_t *)q;
+    a.ends = ends;
+    a.lens = lens;
+    a.table = table;
+    a.out = out;
+    a.lse = lse;
+    a.q_stride = q_stride;
+    a.table_stride = table_width;
+    a.c = scale * 1.4426950408889634f;
+    a.seqs = (int)seqs;
+    a.tokens = (int)tokens;
+    a.heads = (int)cache->kv_heads;
+    a.group = (int)group;
+    a.page_shift = log2_of(cache->page_size);
+    a.pages = (int)cache->pages;
+    a.table_width = (int)table_width;
+    a.causal = causal;
+    a.window = (int)std::min<int64_t>(window, 1 << 30);
+    a.out_kind = out_dtype;
+    for (int i = 0; i < plan.n; ++i) {
+        const AttnKernel k = attn_kernel(plan.which[i], cache->is_fp4 != 0, (int)cache->head_dim);
+        const bool parts = split && plan.bytes[i] > 0;
+        a.counters = parts ? (unsigned *)workspace : nullptr;
+        a.parts = parts ? (uint8_t *)workspace + kSplitCounters * sizeof(unsigned) : nullptr;
+        a.rows_above = plan.above[i];
+        a.rows_upto = plan.upto[i];
+        a.target = k.target;
+        const int64_t grid = plan.base[i] + (parts ? k.target : 0);
+        if (grid > INT32_MAX)
+            return MXG_ERR_SHAPE;
+        hipLaunchKernelGGL(k.fn, dim3((unsigned)grid), dim3(256), 0, (hipStream_t)stream, a);
+        rc = host_hip_status(hipGetLastError());
+        if (rc)
+            return rc;
+    }
+    return MXG_OK;
+}
+
+}  // extern "C"

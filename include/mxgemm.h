@@ -333,6 +333,144 @@ int64_t mx_fused_variant_max_k(int variant, int is_fp4);
 int mx_dense_gemm(int dtype, int trans_a, int trans_b, const void *a, const void *b, void *c,
                   int64_t M, int64_t N, int64_t K, int out_dtype, mxg_stream_t stream);
 
+/*
+ * The operators around the products of a transformer layer in MX formats:
+ * RMSNorm into the next product's A operand, a paged key/value cache held
+ * in MX codes, and the attention of new tokens over that cache.  Same
+ * ownership, stream and error contract as above: nothing is allocated,
+ * arguments are checked before any HIP call, work is enqueued on `stream`.
+ */
+
+/*
+ * RMSNorm of BF16 rows, with the residual's addition before it.  Per row:
+ *
+ *   h = x + residual            rounded to BF16 (h = x without a residual)
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ *
+ * x, residual  BF16 [rows][K]; residual NULL: none.
+ * weight       BF16 [K], or NULL for ones.
+ * h            output, BF16 [rows][K], or NULL: not written.  May be x or
+ *              residual (a residual stream updated in place).
+ * y, y_scale   output.  out_kind MXG_OUT_BF16 / F16 / F32: y [rows][K] of
+ *              that type, y_scale ignored.  MXG_OUT_MXFP8 / MXFP4: y rounded
+ *              to BF16 and quantized exactly as mx_quantize_bf16 does, codes
+ *              [rows][K] or [rows][K/2] into y and E8M0 codes [rows][K/32]
+ *              into y_scale: the A operand of a following MX GEMM.
+ * rows, K      rows >= 0 (0: nothing is enqueued, pointers may be NULL); K a positive multiple of
+ *              32, at most 65536.
+ * eps          >= 0, finite.
+ *
+ * The sum of squares is taken in FP64.  A row that holds a NaN or an
+ * infinity gives NaN (scale codes 0xFF), as the formula does.
+ * MXG_ERR_NULL, MXG_ERR_DTYPE (out_kind), MXG_ERR_SHAPE, MXG_ERR_K_ALIGN
+ * (K % 32), MXG_ERR_CONFIG (eps), MXG_ERR_PTR_ALIGN (every pointer but
+ * y_scale 16-byte aligned), MXG_ERR_DEVICE, MXG_ERR_HIP.
+ */
+int mx_rmsnorm(const void *x, const void *residual, const void *weight, void *h, void *y, void *y_scale,
+               int64_t rows, int64_t K, float eps, int out_kind, mxg_stream_t stream);
+
+/*
+ * A paged key/value cache in MX formats: pages of page_size tokens, within
+ * a page head by head, blocks of 32 along the head dimension.
+ *
+ * k_codes, v_codes    [pages][kv_heads][page_size][head_dim] E4M3 bytes, or
+ *                     [..][head_dim/2] E2M1 pairs (is_fp4); 16-byte aligned.
+ * k_scales, v_scales  [pages][kv_heads][page_size][head_dim/32] E8M0 codes;
+ *                     4-byte aligned.
+ * page_size           a power of two, at most 65536.
+ * head_dim            a multiple of 32, at most 1024.
+ *
+ * Slot s of the cache is token s % page_size of page s / page_size.  Any
+ * content is valid: slots that were never written may hold anything.
+ */
+typedef struct {
+    void *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t pages, page_size, kv_heads, head_dim;
+    int is_fp4;
+} mxg_kv_cache_t;
+
+/*
+ * Write tokens into the cache, quantized as mx_quantize_bf16 does, and read
+ * slots back as BF16 (element times scale; exact, but for blocks of subnormal
+ * BF16 values, which round to nearest even; NaN for scale code 0xFF).
+ *
+ * k, v       BF16, token t at element t * k_stride / t * v_stride, its
+ *            kv_heads * head_dim values contiguous (so parts of the rows of a
+ *            joint QKV product are taken as they are).  16-byte aligned,
+ *            strides multiples of 8 and at least kv_heads * head_dim.
+ * slots      DEVICE memory, int64 [tokens], 8-byte aligned: each token's
+ *            slot.  A slot outside the cache (-1, for padding) is skipped by
+ *            a write and reads zeros.  Two tokens written to one slot leave
+ *            either's values, block by block.
+ * tokens     >= 0 (0: nothing is enqueued, k, v, slots may be NULL); tokens * kv_heads * head_dim
+ *            at most 2^33.
+ *
+ * MXG_ERR_NULL, MXG_ERR_SHAPE, MXG_ERR_K_ALIGN (head_dim % 32, a stride % 8),
+ * MXG_ERR_PTR_ALIGN, MXG_ERR_DEVICE, MXG_ERR_HIP.
+ */
+int mx_kv_cache_write(const mxg_kv_cache_t *cache, const void *k, const void *v, int64_t k_stride,
+                      int64_t v_stride, const int64_t *slots, int64_t tokens, mxg_stream_t stream);
+int mx_kv_cache_read(const mxg_kv_cache_t *cache, void *k, void *v, int64_t k_stride, int64_t v_stride,
+                     const int64_t *slots, int64_t tokens, mxg_stream_t stream);
+
+/*
+ * Attention of each sequence's new tokens (one, a few, or a chunk of a
+ * prompt) over its keys and values in a paged cache, which hold the new
+ * tokens' own too (write them first).  For query head hq of new token i of n
+ * of a sequence of L keys, KV head hq / (q_heads / kv_heads), position
+ * pos = L - n + i:
+ *
+ *   x_j = scale * q . k_j   for the keys j it sees: j < L, with causal
+ *                           j <= pos, with a window > 0 also j > pos - window
+ *   lse = log sum_j exp(x_j),   out = sum_j exp(x_j - lse) v_j
+ *
+ * q           BF16, token t at element t * q_stride, its [q_heads][head_dim]
+ *             values contiguous; 16-byte aligned, q_stride a multiple of 8.
+ * ends        DEVICE int32 [seqs]: the end of each sequence's rows of q
+ *             (cumulative), as mx_grouped_mm_*'s offs.
+ * lens        DEVICE int32 [seqs]: keys L of each sequence, new ones included.
+ * table       DEVICE int32 [seqs][table_width]: the page of keys
+ *             [i * page_size, (i + 1) * page_size).  Entries past a
+ *             sequence's keys are not looked at.
+ * tokens      rows of q (and of out); q_heads a multiple of kv_heads.
+ * max_new     the most new tokens of a sequence: chooses kernels, for speed
+ *             only (any value gives the same results).
+ * scale       > 0, finite (usually 1 / sqrt(head_dim)).
+ * out         [tokens][q_heads][head_dim] of out_dtype (BF16, FP16, FP32),
+ *             contiguous, 16-byte aligned.
+ * lse         FP32 [tokens][q_heads], or NULL.
+ * workspace   optional device memory, 16-byte aligned, for splitting long
+ *             key ranges over workgroups: mx_paged_attention_workspace_bytes
+ *             bytes, its first 64 KiB zero when it is allocated and left zero
+ *             by every call (one workspace serves these calls and the split-K
+ *             products of a stream).  NULL or too small: no splitting, the
+ *             same results but for FP32 rounding, slower for few long
+ *             sequences.
+ *
+ * Any content of ends, lens, table and the cache gives in-bounds accesses:
+ * ends are clamped to [previous end, tokens], lens to [0, table_width *
+ * page_size]; keys on a page outside [0, pages) are as if they were not
+ * there.  A row that sees no key gives zeros and lse = -inf.  Rows of q past
+ * the last end are not written.  NaN among a key's values reaches only the
+ * rows that see the key.  head_dim is 64 or 128.  p = exp(x - reference) is
+ * rounded to BF16 for its product with the values; all sums are FP32.
+ *
+ * MXG_ERR_NULL, MXG_ERR_DTYPE (out_dtype), MXG_ERR_SHAPE (sizes; seqs or
+ * q_heads above 65536; tokens * q_heads above 2^30; table_width * page_size
+ * above 2^30; head_dim), MXG_ERR_K_ALIGN (head_dim % 32, q_stride % 8),
+ * MXG_ERR_CONFIG (scale, causal), MXG_ERR_PTR_ALIGN, MXG_ERR_DEVICE,
+ * MXG_ERR_HIP.
+ */
+int mx_paged_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, const int32_t *ends,
+                       const int32_t *lens, const int32_t *table, int64_t table_width, int64_t seqs,
+                       int64_t tokens, int64_t q_heads, int64_t max_new, float scale, int causal,
+                       int64_t window, void *out, int out_dtype, float *lse, void *workspace,
+                       size_t workspace_bytes, mxg_stream_t stream);
+/* Workspace bytes mx_paged_attention splits with for these sizes (any
+ * lengths); 0 where it does not split, or for invalid arguments. */
+size_t mx_paged_attention_workspace_bytes(const mxg_kv_cache_t *cache, int64_t seqs, int64_t tokens,
+                                          int64_t q_heads, int64_t max_new);
+
 /* The configuration the default entry points pick for a shape: returns the
  * variant (>= 0) and stores the K-part count in *splits (if not NULL), for
  * a call given a large enough workspace (with_workspace = 1) or none (0);
