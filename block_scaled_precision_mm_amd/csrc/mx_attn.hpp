@@ -45,9 +45,9 @@
 // values of slots past the sequence's end or on pages outside the cache are
 // replaced by zeros as they are expanded.  A NaN among the values of a key
 // that some rows of a tile see and others do not would reach the others as
-// 0 * NaN: such a tile (rare; found as it is expanded) runs its second
-// product on the values without the NaNs, and again on their indicator to
-// poison exactly the rows that see them.
+// 0 * NaN: in tiles that not every row sees whole, NaNs become zeros as they
+// are expanded, and where there was one (rare) the rows that see it get
+// their NaNs from the codes themselves (attn_poison).
 #pragma once
 
 #include "mx_cache.hpp"
@@ -71,11 +71,12 @@ struct AttnArgs {
     long long q_stride, table_stride;
     float c;                                // scale * log2 e
     int seqs, tokens, heads, group;         // KV heads, query heads per KV head
+    FastDiv by_heads, by_group;
     int page_shift, pages, table_width;
     int causal, window;
     int out_kind;
     int rows_above, rows_upto;              // the sequences of this launch: rows_above < n * group <= rows_upto
-    int target;                             // resident workgroups
+    float per_target;                       // KV heads / workgroups that can run at once
 };
 
 // One workgroup's work.
@@ -90,8 +91,29 @@ struct AttnItem {
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// A sequence as lane l of chunk c0 sees it: row tiles and key tiles of the
-// sequences of this launch's class, 0 row tiles for others.
+// Inclusive sums over the wave's lanes (DPP row shifts and broadcasts).
+template <class T, int CTRL, int ROWS>
+__device__ __forceinline__ T dpp_or_0(T v)
+{
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, false));
+}
+
+template <class T>
+__device__ __forceinline__ T wave_prefix(T v)
+{
+    v += dpp_or_0<T, 0x111, 0xF>(v);
+    v += dpp_or_0<T, 0x112, 0xF>(v);
+    v += dpp_or_0<T, 0x114, 0xF>(v);
+    v += dpp_or_0<T, 0x118, 0xF>(v);
+    v += dpp_or_0<T, 0x142, 0xA>(v);
+    v += dpp_or_0<T, 0x143, 0xC>(v);
+    return v;
+}
+
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// A sequence as a lane sees it: row tiles and key tiles of the sequences of
+// this launch's class, 0 row tiles for others.
 struct AttnSeq {
     int tok0, ntok, len, rtiles, ktiles;
 };
@@ -105,14 +127,13 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &p, int s, int &carry
     const int lane = threadIdx.x & 63;
     AttnSeq q = {0, 0, 0, 0, 0};
     int end = carry;
-    if (s < p.seqs) {
+    const bool mine = s < p.seqs;
+    if (mine) {
         end = min(max(p.ends[s], carry), p.tokens);
-        const long long most = (long long)p.table_width << p.page_shift;
-        q.len = (int)min((long long)max(p.lens[s], 0), most);
+        q.len = min(max(p.lens[s], 0), p.table_width << p.page_shift);
     }
     int before = __shfl_up(end, 1);
     before = lane ? before : carry;
-    const bool mine = s < p.seqs;
     if (__any(mine && end < before)) {
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
@@ -122,7 +143,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &p, int s, int &carry
         before = __shfl_up(end, 1);
         before = lane ? before : carry;
     }
-    carry = uniform(__shfl(end, 63));
+    carry = lane_value(end, 63);
     q.tok0 = before;
     q.ntok = mine ? end - before : 0;
     const int rows = q.ntok * p.group;
@@ -135,97 +156,90 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &p, int s, int &carry
     return q;
 }
 
-template <class T>
-__device__ __forceinline__ T wave_sum(T v)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        v += __shfl_xor(v, d);
-    return v;
-}
-
-__device__ __forceinline__ int wave_prefix(int v)   // inclusive
-{
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int u = __shfl_up(v, d);
-        v += lane >= d ? u : 0;
-    }
-    return v;
-}
+__device__ __forceinline__ int cdiv_u(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1u) / (unsigned)b); }
 
 // Find workgroup `blockIdx.x`'s item; false if it has none.  Every wave of
 // the workgroup computes it (all results are wave-uniform).  min_tiles: the
 // fewest key tiles worth a part of their own.
+//
+// A sequence's key tiles are cut into parts of at most `chunk`, where chunk
+// is at least the total of (row tile, key tile) pairs over the number of
+// workgroups that can run at once: split row tiles then have fewer than
+// twice that number of parts in all, which bounds the workspace, and the
+// items are at most one per row tile and that number more, which bounds the
+// grid (the factor keeps both with the FP32 total's rounding).
 template <int BM, int BN>
 __device__ __forceinline__ bool plan_item(const AttnArgs &p, int min_tiles, AttnItem &it)
 {
     const int lane = threadIdx.x & 63;
-    int chunk = 0x7FFFFFFF, carry = 0;
+    int chunk = 1 << 30, carry = 0;
     AttnSeq q = attn_seq<BM, BN>(p, lane, carry);
     const int carry64 = carry;
     if (p.counters) {
-        long long total = (long long)q.rtiles * q.ktiles;
+        float total = (float)q.rtiles * (float)q.ktiles;
         for (int s0 = 64; s0 < p.seqs; s0 += 64) {
             const AttnSeq r = attn_seq<BM, BN>(p, s0 + lane, carry);
-            total += (long long)r.rtiles * r.ktiles;
+            total += (float)r.rtiles * (float)r.ktiles;
         }
-        total = wave_sum(total) * p.heads;
-        const long long c = (total + p.target - 1) / p.target;
-        chunk = (int)min(max(c, (long long)min_tiles), (long long)0x7FFFFFFF);
-        chunk = uniform(chunk);
+        total = __int_as_float(lane_value(__float_as_int(wave_prefix(total)), 63)) * p.per_target * 1.001f;
+        chunk = max(uniform((int)fminf(total, 1e9f) + 1), min_tiles);
     }
     carry = carry64;
-    int item = blockIdx.x, slots = 0, tiles = 0;      // before the chunk of sequences looked at
+    int item = blockIdx.x, slots = 0, tiles = 0;      // before the 64 sequences looked at
     for (int s0 = 0;; s0 += 64) {
         if (s0 >= p.seqs)
             return false;
         if (s0 > 0)
             q = attn_seq<BM, BN>(p, s0 + lane, carry);
-        const int parts = max(1, q.ktiles / chunk + (q.ktiles % chunk != 0));
+        const int parts = max(1, cdiv_u(q.ktiles, chunk));
         const int mytiles = p.heads * q.rtiles, mine = mytiles * parts;
-        const int upto = wave_prefix(mine);
-        const int all = uniform(__shfl(upto, 63));
+        const int upto = wave_prefix(mine), slots_upto = wave_prefix(parts > 1 ? mine : 0), tiles_upto = wave_prefix(mytiles);
+        const int all = lane_value(upto, 63);
         if (item >= all) {
             item -= all;
-            slots += uniform(wave_sum(parts > 1 ? mine : 0));
-            tiles += uniform(wave_sum(mytiles));
+            slots += lane_value(slots_upto, 63);
+            tiles += lane_value(tiles_upto, 63);
             continue;
         }
         const int at = __ffsll((unsigned long long)__ballot(item < upto)) - 1;
-        const int before_slots = wave_sum(lane < at && parts > 1 ? mine : 0);
-        const int before_tiles = wave_sum(lane < at ? mytiles : 0);
         it.seq = s0 + at;
-        it.tok0 = uniform(__shfl(q.tok0, at));
-        it.ntok = uniform(__shfl(q.ntok, at));
-        it.len = uniform(__shfl(q.len, at));
-        const int rtiles = uniform(__shfl(q.rtiles, at)), sparts = uniform(__shfl(parts, at));
-        item -= uniform(__shfl(upto - mine, at));
+        it.tok0 = lane_value(q.tok0, at);
+        it.ntok = lane_value(q.ntok, at);
+        it.len = lane_value(q.len, at);
+        const int rtiles = lane_value(q.rtiles, at), sparts = lane_value(parts, at), smine = lane_value(mine, at);
+        item -= lane_value(upto, at) - smine;
+        slots += lane_value(slots_upto, at) - (sparts > 1 ? smine : 0);
+        tiles += lane_value(tiles_upto, at) - p.heads * rtiles;
         // heads innermost: the workgroups of a head, which share its keys,
         // are then apart by the number of heads and (with 8) on one XCD
-        it.head = item % p.heads;
-        const int rest = item / p.heads;
+        const int rest = p.by_heads.div(item);
+        it.head = item - rest * p.heads;
+        it.part = rtiles == 1 ? rest : (int)((unsigned)rest / (unsigned)rtiles);
         // the last row tiles of a causal chunk see the most keys: first
-        const int rt = rtiles - 1 - rest % rtiles;
-        it.part = rest / rtiles;
+        const int rt = rtiles - 1 - (rest - it.part * rtiles);
         it.row0 = rt * BM;
-        it.counter = tiles + uniform(before_tiles) + rt * p.heads + it.head;
-        it.slot = slots + uniform(before_slots) + rt * p.heads + it.head;
+        it.counter = tiles + rt * p.heads + it.head;
+        it.slot = slots + rt * p.heads + it.head;
         it.slot_step = rtiles * p.heads;
-        // the keys that some row of the tile sees
-        const int t0 = it.row0 / p.group, t1 = min((it.row0 + BM - 1) / p.group, it.ntok - 1);
+        // the keys that some row of the tile sees, and those that all do
+        const int t0 = p.by_group.div(it.row0), t1 = min(p.by_group.div(it.row0 + BM - 1), it.ntok - 1);
         const int pos0 = it.len - it.ntok + t0, pos1 = it.len - it.ntok + t1;
         const int hi = p.causal ? min(max(pos1 + 1, 0), it.len) : it.len;
         const int lo = p.window > 0 ? min(max(pos0 - p.window + 1, 0), hi) : 0;
         it.all_lo = p.window > 0 ? max(pos1 - p.window + 1, 0) : 0;
         it.all_hi = p.causal ? min(max(pos0 + 1, 0), it.len) : it.len;
         const int k0 = lo / BN, nt = (hi + BN - 1) / BN - k0;
-        it.parts = min(sparts, max(1, nt / chunk + (nt % chunk != 0)));
+        it.parts = sparts == 1 ? 1 : min(sparts, max(1, cdiv_u(nt, chunk)));
         if (it.part >= it.parts)
             return false;
-        it.key0 = (k0 + (int)((long long)nt * it.part / it.parts)) * BN;
-        it.key1 = min(hi, (k0 + (int)((long long)nt * (it.part + 1) / it.parts)) * BN);
+        it.key0 = k0 * BN;
+        it.key1 = hi;
+        if (it.parts > 1) {
+            const int each = (int)((unsigned)nt / (unsigned)it.parts), more = nt - each * it.parts;
+            const int first = each * it.part + min(it.part, more);
+            it.key0 = (k0 + first) * BN;
+            it.key1 = min(hi, it.key0 + (each + (it.part < more)) * BN);
+        }
         return true;
     }
 }
@@ -239,7 +253,7 @@ struct AttnRow {
 __device__ __forceinline__ AttnRow attn_row(const AttnArgs &p, const AttnItem &it, int row)
 {
     AttnRow r;
-    const int token = row / p.group;
+    const int token = p.by_group.div(row);
     r.head = row - token * p.group;
     r.token = token < it.ntok ? token : -1;
     const int pos = it.len - it.ntok + token;
@@ -248,27 +262,14 @@ __device__ __forceinline__ AttnRow attn_row(const AttnArgs &p, const AttnItem &i
     return r;
 }
 
-// Geometry of KT keys of codes, loaded 16 bytes per lane by NTHR threads:
-// CH chunks per key, chunk (tid % CH) of key tid / CH + j * KPL in load j
-// (threads from KPL * CH on load nothing).
-template <int F, int D, int KT, int NTHR>
+// Rows of codes and scales, and the 16-byte chunks of a row.
+template <int F, int D>
 struct AttnGeom {
     static constexpr int RB = F == FMT_FP4 ? D / 2 : D;     // bytes of a key's codes
     static constexpr int SB = D / 32;                       // and of its scales
-    static constexpr int CH = RB / 16;
+    static constexpr int CH = RB / 16;                      // chunks of a key
     static constexpr int VC = F == FMT_FP4 ? 32 : 16;       // values of a chunk
-    static constexpr int KPL = NTHR / CH < KT ? NTHR / CH : KT;   // keys per load
-    static constexpr bool ALL = KPL * CH == NTHR;           // every thread loads
-    static constexpr int NL = KT / KPL;                     // loads per thread
-    static_assert(KT % KPL == 0 && NL >= 1, "whole loads");
-};
-
-// Codes, scale codes and validity of this thread's chunks of a tile of keys.
-template <class G>
-struct AttnTileRegs {
-    u4v k[G::NL], v[G::NL];
-    unsigned ks[G::NL], vs[G::NL];      // scale code of the chunk
-    bool ok[G::NL];
+    static constexpr int NP = VC / 8;                       // pieces of eight
 };
 
 // Page of key `key` of a sequence (its table row), or -1 past key1 or where
@@ -289,22 +290,7 @@ __device__ __forceinline__ long long attn_row_at(const AttnArgs &p, int page, in
     return page >= 0 ? ((((long long)page * p.heads + head) << p.page_shift) + off) : 0;
 }
 
-template <class G>
-__device__ __forceinline__ void attn_load(const AttnArgs &p, int head, int key, int chunk, const int (&page)[G::NL],
-                                          AttnTileRegs<G> &r)
-{
-#pragma unroll
-    for (int j = 0; j < G::NL; ++j) {
-        r.ok[j] = page[j] >= 0;
-        const long long at = attn_row_at(p, page[j], head, key + j * G::KPL);
-        r.k[j] = *reinterpret_cast<const u4v *>(p.codes[0] + at * G::RB + 16 * chunk);
-        r.v[j] = *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + 16 * chunk);
-        r.ks[j] = p.scales[0][at * G::SB + chunk * G::VC / 32];
-        r.vs[j] = p.scales[1][at * G::SB + chunk * G::VC / 32];
-    }
-}
-
-// A chunk as BF16: VC / 8 pieces of eight values.
+// A chunk as BF16, in pieces of eight values.
 template <int F, int NP>
 __device__ __forceinline__ void attn_expand(const u4v &c, unsigned s, u4v (&w)[NP])
 {
@@ -318,48 +304,64 @@ __device__ __forceinline__ void attn_expand(const u4v &c, unsigned s, u4v (&w)[N
     }
 }
 
-// Whether a chunk holds a NaN.
-template <int F>
-__device__ __forceinline__ bool attn_has_nan(const u4v &c, unsigned s)
+__device__ __forceinline__ bool bf16_nan(unsigned x) { return (x & 0x7FFFu) > 0x7F80u; }
+
+// A chunk of values of a tile that not every row sees whole: zeros for a key
+// that is not there and in the place of NaNs.  Returns whether there was one.
+template <int NP>
+__device__ __forceinline__ bool attn_clean(u4v (&w)[NP], bool ok)
 {
-    bool nan = s == 255u;
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < NP; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool a = bf16_nan(w[e][i]), b = bf16_nan(w[e][i] >> 16);
+            nan |= a | b;
+            w[e][i] = ok ? w[e][i] & ((a ? 0u : 0xFFFFu) | (b ? 0u : 0xFFFF0000u)) : 0u;
+        }
+    return nan && ok;
+}
+
+// Four consecutive values d .. d + 3 of a row of the cache: bit i set where
+// value d + i is a NaN.
+template <int F, int D>
+__device__ __forceinline__ unsigned attn_nan4(const AttnArgs &p, long long at, int d)
+{
+    using G = AttnGeom<F, D>;
+    unsigned m = p.scales[1][at * G::SB + d / 32] == 255u ? 15u : 0u;
     if constexpr (F == FMT_FP8) {
-        unsigned t = 0;
+        const unsigned c = *reinterpret_cast<const unsigned *>(p.codes[1] + at * G::RB + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            t |= (c[i] & 0x7F7F7F7Fu) + 0x01010101u;
-        nan |= (t & 0x80808080u) != 0;
+            m |= (unsigned)((c >> (8 * i) & 0x7Fu) == 0x7Fu) << i;
     }
-    return nan;
+    return m;
 }
 
-enum { VALUES_PLAIN = 0, VALUES_CLEAN = 1, VALUES_NAN = 2 };   // as they are; NaNs as 0; 1 at NaNs, else 0
-
-__device__ __forceinline__ unsigned bf16_pair_mode(unsigned w, int mode)
+// The rows of this lane that see a key with NaNs among its values get them.
+// keys [key, key + n) of a tile whose NaNs became zeros; group(j, f) calls
+// f(d, v) for its j-th run of four sums v at columns d .. d + 3.
+template <int F, int D, int NG, class Group>
+__device__ __forceinline__ void attn_poison(const AttnArgs &p, const int *table, const AttnItem &it, int key, int n,
+                                            const AttnRow &row, Group &&group)
 {
-    unsigned o = 0;
+    for (int k = key; k < min(key + n, it.key1); ++k) {
+        const int page = attn_page(p, table, k, it.key1);
+        if (page < 0)
+            continue;
+        const long long at = attn_row_at(p, page, it.head, k);
+        const bool see = k >= row.lo && k < row.hi;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const unsigned x = (w >> (16 * h)) & 0xFFFFu;
-        const bool nan = (x & 0x7FFFu) > 0x7F80u;
-        o |= (mode == VALUES_CLEAN ? (nan ? 0u : x) : (nan ? 0x3F80u : 0u)) << (16 * h);
+        for (int j = 0; j < NG; ++j)
+            group(j, [&](int d, float &a, float &b, float &c, float &e) {
+                const unsigned m = see ? attn_nan4<F, D>(p, at, d) : 0u;
+                a = m & 1 ? __builtin_nanf("") : a;
+                b = m & 2 ? __builtin_nanf("") : b;
+                c = m & 4 ? __builtin_nanf("") : c;
+                e = m & 8 ? __builtin_nanf("") : e;
+            });
     }
-    return o;
-}
-
-// A piece of a key's values as the second product takes it: zeros for a key
-// that is not there.
-__device__ __forceinline__ u4v values_mode(u4v w, bool ok, int mode)
-{
-    if (mode != VALUES_PLAIN) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = bf16_pair_mode(w[i], mode);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = ok ? w[i] : 0u;
-    return w;
 }
 
 __device__ __forceinline__ bf16x8v as_bf16x8(u4v v) { return __builtin_bit_cast(bf16x8v, v); }
@@ -370,6 +372,19 @@ __device__ __forceinline__ u2v lds_read_tr(const char *at)
 {
     return __builtin_bit_cast(
         u2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4v *)at));
+}
+
+// max over the two lanes l, l ^ 32 (l ^ 16), without LDS.
+__device__ __forceinline__ float max_across_32(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ float max_across_16(float v)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 constexpr float kRescale = 8.0f;
@@ -392,10 +407,12 @@ __device__ __forceinline__ void attn_store8(const AttnArgs &p, size_t row, int d
 }
 
 // Bytes of the workspace slot of a part of a tile of `rows` rows (a multiple
-// of 128 bytes; sums of 256 threads' runs of eight).
+// of 128 bytes): the threads' runs of eight sums, 512 threads from 256 rows
+// on and 256 below, and (m, l) of each row.
 constexpr int attn_slot_bytes(int rows, int dim)
 {
-    return cdiv_c(rows * dim / 8, 256) * 256 * 32 + cdiv_c(rows * 8, 128) * 128;
+    const int threads = rows >= 256 ? 512 : 256;
+    return cdiv_c(rows * dim / 8, threads) * threads * 32 + cdiv_c(rows * 8, 128) * 128;
 }
 
 // The end of a row tile.  Its NR x D sums lie with the threads of the
@@ -470,7 +487,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
             continue;
         const int row = (tid + u * NTHR) / RUNS;
         float f[8] = {0, 0, 0, 0, 0, 0, 0, 0}, m = -__builtin_inff(), l = 0.0f;
-        constexpr int PF = 4;       // parts in flight
+        constexpr int PF = 8;       // parts in flight
         for (int q0 = 0; q0 < it.parts; q0 += PF) {
             u4v a[PF], b[PF];
             u2v ml[PF];
@@ -523,13 +540,17 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
 // so the reads are contiguous), then, in the same place, the values' tile
 // as rows of 2D + 32 bytes (the 32 spread the four keys and four lane groups
 // of a transposing read over the banks).
-template <int F, int D, int QT>
-__global__ __launch_bounds__(256)
+//
+// PAGED: pages hold at least the KPL keys of one load instruction, so the
+// page is a scalar and the lanes' offsets are the same for every tile.
+template <int F, int D, int QT, int PAGED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(QT == 1 ? 3 : 2)))
 void mx_attn_rows(AttnArgs p)
 {
     constexpr int KT = 32, BM = 16 * QT, BN = 4 * KT;
-    using G = AttnGeom<F, D, KT, 64>;
-    constexpr int KS = D / 32, DT = D / 16, NP = G::VC / 8;
+    using G = AttnGeom<F, D>;
+    constexpr int KS = D / 32, DT = D / 16, NP = G::NP;
+    constexpr int KPL = 64 / G::CH, NL = KT / KPL;      // keys per load, loads per tile
     constexpr int KBYTES = 2 * KS * 1024, VROW = 2 * D + 32, VBYTES = KT * VROW;
     constexpr int WBYTES = KBYTES > VBYTES ? KBYTES : VBYTES;
     constexpr int OROW = D + 4;                         // floats of a row of sums in LDS
@@ -543,9 +564,13 @@ void mx_attn_rows(AttnArgs p)
     if (!plan_item<BM, BN>(p, 1, it))
         return;
 
+    const int *table = p.table + it.seq * p.table_stride;
+    const int mykey = lane / G::CH, chunk = lane % G::CH;
+    int key = it.key0 + wave * KT;
+    int page = attn_page(p, table, key + (lane & 31), it.key1);     // of key `lane & 31` of the next tile loaded
+
     AttnRow row[QT];
     bf16x8v q[QT][KS];
-    int lo_most = 0, hi_least = 0x7FFFFFFF;             // keys that every row of the tile sees
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         row[t] = attn_row(p, it, it.row0 + 16 * t + r);
@@ -554,22 +579,9 @@ void mx_attn_rows(AttnArgs p)
 #pragma unroll
         for (int s = 0; s < KS; ++s)
             q[t][s] = as_bf16x8(row[t].token >= 0 ? *reinterpret_cast<const u4v *>(src + 32 * s) : u4v{0u, 0u, 0u, 0u});
-        if (row[t].token >= 0) {
-            lo_most = max(lo_most, row[t].lo);
-            hi_least = min(hi_least, row[t].hi);
-        }
     }
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) {
-        lo_most = max(lo_most, __shfl_xor(lo_most, d));
-        hi_least = min(hi_least, __shfl_xor(hi_least, d));
-    }
-    lo_most = uniform(lo_most);
-    hi_least = uniform(hi_least);
 
     char *mem = lds + wave * WBYTES;
-    const int *table = p.table + it.seq * p.table_stride;
-    const int mykey = lane / G::CH, chunk = lane % G::CH;
     v4f o[QT][DT];
     float m[QT], l[QT];
 #pragma unroll
@@ -581,119 +593,96 @@ void mx_attn_rows(AttnArgs p)
             o[t][d] = v4f{0, 0, 0, 0};
     }
 
-    AttnTileRegs<G> cur;
-    int page[G::NL];
-    auto pages_of = [&](int key) {
+    // codes and scale codes of this lane's chunks of the next tile, and the
+    // keys of it that are there (bits)
+    u4v kc[NL], vc[NL];
+    unsigned ks[NL], vs[NL], there = 0;
+    const unsigned voff = mykey * G::RB + chunk * 16, soff = mykey * G::SB + chunk * G::VC / 32;
+    auto load = [&](int k) {
+        there = (unsigned)__ballot(page >= 0);
 #pragma unroll
-        for (int j = 0; j < G::NL; ++j)
-            page[j] = attn_page(p, table, key + mykey + j * G::KPL, it.key1);
-    };
-    int key = it.key0 + wave * KT;
-    if (key < it.key1) {
-        pages_of(key);
-        attn_load<G>(p, it.head, key + mykey, chunk, page, cur);
-        pages_of(key + BN);
-    }
-    auto store_values = [&](int j, const u4v &codes, unsigned scale, bool ok, int mode) {
-        u4v w[NP];
-        attn_expand<F>(codes, scale, w);
-        char *at = mem + (mykey + j * G::KPL) * VROW + chunk * G::VC * 2;
-#pragma unroll
-        for (int e = 0; e < NP; ++e)
-            *reinterpret_cast<u4v *>(at + 16 * e) = values_mode(w[e], ok, mode);
+        for (int j = 0; j < NL; ++j) {
+            if constexpr (PAGED) {
+                // scalar row of the first key of the load
+                const long long at = attn_row_at(p, lane_value(page, j * KPL), it.head, k + j * KPL);
+                kc[j] = *reinterpret_cast<const u4v *>(p.codes[0] + at * G::RB + voff);
+                vc[j] = *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + voff);
+                ks[j] = p.scales[0][at * G::SB + soff];
+                vs[j] = p.scales[1][at * G::SB + soff];
+            } else {
+                const long long at = attn_row_at(p, __shfl(page, mykey + j * KPL), it.head, k + mykey + j * KPL);
+                kc[j] = *reinterpret_cast<const u4v *>(p.codes[0] + at * G::RB + chunk * 16);
+                vc[j] = *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + chunk * 16);
+                ks[j] = p.scales[0][at * G::SB + chunk * G::VC / 32];
+                vs[j] = p.scales[1][at * G::SB + chunk * G::VC / 32];
+            }
+        }
+        page = attn_page(p, table, k + BN + (lane & 31), it.key1);
     };
     auto wave_fence = [] {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     };
+    if (key < it.key1)
+        load(key);
+    // piece (chunk * NP + e) of a key's D / 8 is one lane's operand of one step
+    char *kput = mem + (((chunk * NP) >> 2) * 64 + ((chunk * NP) & 3) * 16) * 16;
+    char *vput = mem + mykey * VROW + chunk * G::VC * 2;
     const char *vread = mem + (4 * g + (r >> 2)) * VROW + (r & 3) * 8;
-    // values of keys 4g .. and 16 + 4g .., columns 16 d + r
-    auto values_at = [&](int d) {
-        const u2v a = lds_read_tr(vread + 32 * d), b = lds_read_tr(vread + 16 * VROW + 32 * d);
-        return as_bf16x8(u4v{a.x, a.y, b.x, b.y});
-    };
     for (; key < it.key1; key += BN) {
-        // keys into LDS: chunk (key kk, values VC chunk ..) is pieces of eight
-        // values, each one lane's operand of one 32-deep step
 #pragma unroll
-        for (int j = 0; j < G::NL; ++j) {
+        for (int j = 0; j < NL; ++j) {
             u4v w[NP];
-            attn_expand<F>(cur.k[j], cur.ks[j], w);
-            const int kk = mykey + j * G::KPL;
+            attn_expand<F>(kc[j], ks[j], w);
+            const int kk = mykey + j * KPL;
 #pragma unroll
-            for (int e = 0; e < NP; ++e) {
-                const int piece = chunk * NP + e;       // of the key's D / 8
-                *reinterpret_cast<u4v *>(mem + (((kk >> 4) * KS + (piece >> 2)) * 64 + (piece & 3) * 16 + (kk & 15)) * 16) = w[e];
-            }
+            for (int e = 0; e < NP; ++e)
+                *reinterpret_cast<u4v *>(kput + ((kk >> 4) * KS * 64 + e * 16 + (kk & 15)) * 16) = w[e];
         }
         wave_fence();
         v4f x[QT][2];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
+            for (int kt = 0; kt < 2; ++kt) {
                 const bf16x8v f = as_bf16x8(*reinterpret_cast<const u4v *>(mem + ((kt * KS + s) * 64 + lane) * 16));
 #pragma unroll
                 for (int t = 0; t < QT; ++t)
                     x[t][kt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[t][s], s ? x[t][kt] : v4f{0, 0, 0, 0}, 0, 0, 0);
             }
         wave_fence();
-        // values into the same place, and the next tile's codes on their way
-        bool ok = true, nan = false;
+        // values into the same place, then the next tile's codes on their way
+        const bool whole = there == 0xFFFFFFFFu && key >= it.all_lo && key + KT <= it.all_hi;
+        const unsigned here = there;
+        bool nan = false;
 #pragma unroll
-        for (int j = 0; j < G::NL; ++j) {
-            ok &= cur.ok[j];
-            nan |= attn_has_nan<F>(cur.v[j], cur.vs[j]) && cur.ok[j];
+        for (int j = 0; j < NL; ++j) {
+            u4v w[NP];
+            attn_expand<F>(vc[j], vs[j], w);
+            if (!whole)
+                nan |= attn_clean(w, here >> (mykey + j * KPL) & 1);
+#pragma unroll
+            for (int e = 0; e < NP; ++e)
+                *reinterpret_cast<u4v *>(vput + j * KPL * VROW + 16 * e) = w[e];
         }
-        const bool whole = __all(ok) && key >= lo_most && key + KT <= hi_least;
-        const bool careful = !whole && __any(nan);
-#pragma unroll
-        for (int j = 0; j < G::NL; ++j)
-            store_values(j, cur.v[j], cur.vs[j], cur.ok[j], careful ? VALUES_CLEAN : VALUES_PLAIN);
-        unsigned vis[QT];                   // bit 4 kt + i: the row sees key 16 kt + 4g + i
-#pragma unroll
-        for (int t = 0; t < QT; ++t)
-            vis[t] = 0xFFu;
-        if (!whole) {
-            unsigned here = 0;              // the lane that loaded a key's first chunk knows
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int kk = 16 * (e >> 2) + 4 * g + (e & 3);
-#pragma unroll
-                for (int j = 0; j < G::NL; ++j) {
-                    const int v = __shfl((int)cur.ok[j], (kk % G::KPL) * G::CH);
-                    here |= (unsigned)(kk / G::KPL == j && v) << e;
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < QT; ++t) {
-                vis[t] = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int k = key + 16 * (e >> 2) + 4 * g + (e & 3);
-                    vis[t] |= (unsigned)(k >= row[t].lo && k < row[t].hi) << e;
-                }
-                vis[t] &= here;
-            }
-        }
-        if (key + BN < it.key1) {
-            attn_load<G>(p, it.head, key + BN + mykey, chunk, page, cur);
-            pages_of(key + 2 * BN);
-        }
+        if (key + BN < it.key1)
+            load(key + BN);
         bf16x8v pb[QT];
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             if (!whole) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    x[t][e >> 2][e & 3] = (vis[t] >> e & 1) ? x[t][e >> 2][e & 3] : -__builtin_inff();
+                for (int e = 0; e < 8; ++e) {
+                    const int kk = 16 * (e >> 2) + 4 * g + (e & 3), k = key + kk;
+                    const bool see = k >= row[t].lo && k < row[t].hi && (here >> kk & 1);
+                    x[t][e >> 2][e & 3] = see ? x[t][e >> 2][e & 3] : -__builtin_inff();
+                }
             }
             float top = -__builtin_inff();
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 top = fmaxf(top, x[t][e >> 2][e & 3]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32)) * p.c;
+            top = max_across_32(max_across_16(top)) * p.c;
             if (__any(top > m[t] + kRescale)) {
                 const float mn = fmaxf(m[t], top);
                 const float w = m[t] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[t] - mn);
@@ -715,42 +704,24 @@ void mx_attn_rows(AttnArgs p)
             }
         }
         wave_fence();
+        // values of keys 4g .. and 16 + 4g .., columns 16 d + r
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-            const bf16x8v f = values_at(d);
+            const u2v a = lds_read_tr(vread + 32 * d), b = lds_read_tr(vread + 16 * VROW + 32 * d);
+            const bf16x8v f = as_bf16x8(u4v{a.x, a.y, b.x, b.y});
 #pragma unroll
             for (int t = 0; t < QT; ++t)
                 o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, pb[t], o[t][d], 0, 0, 0);
         }
         wave_fence();
-        if (careful) {
-            // ones where the values are NaN; a row that sees one gets a NaN there
-#pragma unroll
-            for (int j = 0; j < G::NL; ++j) {
-                const int k = key + mykey + j * G::KPL, pg = attn_page(p, table, k, it.key1);
-                const long long at = attn_row_at(p, pg, it.head, k);
-                store_values(j, *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + 16 * chunk),
-                             p.scales[1][at * G::SB + chunk * G::VC / 32], pg >= 0, VALUES_NAN);
-            }
-            wave_fence();
-            bf16x8v seen[QT];
+        if (!whole && __any(nan)) {
 #pragma unroll
             for (int t = 0; t < QT; ++t)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    seen[t][e] = (vis[t] >> e & 1) ? (__bf16)1.0f : (__bf16)0.0f;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const bf16x8v f = values_at(d);
-#pragma unroll
-                for (int t = 0; t < QT; ++t) {
-                    const v4f bad = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, seen[t], v4f{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o[t][d][i] = bad[i] > 0.0f ? __builtin_nanf("") : o[t][d][i];
-                }
-            }
-            wave_fence();
+                attn_poison<F, D, DT>(p, table, it, key, KT, row[t], [&](int d, auto &&put) {
+                    float a = o[t][d][0], b = o[t][d][1], c = o[t][d][2], e = o[t][d][3];
+                    put(16 * d + 4 * g, a, b, c, e);
+                    o[t][d] = v4f{a, b, c, e};
+                });
         }
     }
 
@@ -822,11 +793,19 @@ void mx_attn_rows(AttnArgs p)
 }
 
 // ------------------------------------------------------------ many rows
-// Row tiles of 128 rows, 32 per wave, over tiles of 64 keys that the four
-// waves expand together into one of two LDS buffers: while tile t is worked
-// on, tile t+1's codes, loaded during tile t-1, are expanded into the other
-// buffer and tile t+2's loads are issued; one barrier per tile.  Bound: MFMA
-// and, next to it, the softmax's VALU work.
+// Row tiles of 32 NW rows, 32 per wave, over tiles of 64 keys that the waves
+// expand together.  A wave alternates between two phases with a barrier after
+// each:
+//     M(t)   the second product of tile t - 1 and the first of tile t: MFMA,
+//            fed from LDS
+//     V(t)   the softmax of tile t, expanding a later tile's codes into
+//            LDS, and the loads of one after that: VALU
+// Bound: MFMA, and next to it the softmax's VALU work.  With NW = 8 the two
+// waves of a SIMD are of different groups (waves 0-3 and 4-7), the second
+// half a step behind the first, so one's M runs beside the other's V; tiles
+// are expanded two ahead (by both groups, one phase apart), which takes three
+// buffers of keys and four of values.  With NW = 4 (fewer rows to waste, two
+// workgroups per CU) one tile ahead, one buffer of keys and two of values.
 //
 // v_mfma_f32_32x32x16_bf16, lane (r = l & 31, h = l >> 5): operands row r,
 // k = 8h .. 8h + 7; accumulator column r, register i row 8 (i >> 2) + 4h +
@@ -835,29 +814,36 @@ void mx_attn_rows(AttnArgs p)
 //
 // LDS of a buffer: the keys as operand fragments (lane order, 1 KB each,
 // apart by 1 KB + 128 bytes so that the expanding stores of a key's steps
-// fall on different banks), then the values as rows of 2D + 64 bytes (the
+// fall on different banks), or the values as rows of 2D + 64 bytes (the
 // four keys and two column groups of a half's transposing read then cover
 // the banks once).
-template <int F, int D>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2)))
+template <int F, int D, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void mx_attn_tile(AttnArgs p)
 {
-    constexpr int BM = 128, BN = 64;
-    using G = AttnGeom<F, D, BN, 256>;
-    constexpr int KS = D / 16, DT = D / 32, NP = G::VC / 8;
+    constexpr int BM = 32 * NW, BN = 64, THR = 64 * NW;
+    using G = AttnGeom<F, D>;
+    constexpr int KS = D / 16, DT = D / 32, NP = G::NP;
+    constexpr int AHEAD = NW == 8 ? 2 : 1, KBUFS = NW == 8 ? 3 : 1, VBUFS = NW == 8 ? 4 : 2;
     constexpr int FS = 1024 + 128, KBYTES = 2 * KS * FS, VROW = 2 * D + 64, VBYTES = BN * VROW;
-    constexpr int BUF = KBYTES + VBYTES;
     constexpr int OROW = D + 4;
-    constexpr int BYTES = 2 * BUF > BM * OROW * 4 ? 2 * BUF : BM * OROW * 4;
+    constexpr int TILES = KBUFS * KBYTES + VBUFS * VBYTES;
+    constexpr int BYTES = TILES > BM * OROW * 4 ? TILES : BM * OROW * 4;
+    // chunk n of the 2 x 64 CH of a tile (keys, then values): thread n % THR
+    constexpr int SIDE = BN * G::CH, NI = cdiv_c(2 * SIDE, THR);
+    constexpr bool EVERY = 2 * SIDE >= THR;
     __shared__ __attribute__((aligned(1024))) char lds[BYTES];
     __shared__ float ml[BM][2];
-    __shared__ unsigned flags[2][4];                    // of each wave's keys: 1 not all there, 2 a NaN among the values
-    __shared__ unsigned char there[2][BN];
+    __shared__ unsigned nans[VBUFS][NW];                // a NaN became a zero in the tile (by wave)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 31, h = lane >> 5;
 
     AttnItem it;
     if (!plan_item<BM, BN>(p, 4, it))
         return;
+
+    const int *table = p.table + it.seq * p.table_stride;
+    const int T = (it.key1 - it.key0 + BN - 1) / BN;
+    int page = attn_page(p, table, it.key0 + lane, it.key1);        // of key `lane` of the next tile loaded
 
     const AttnRow row = attn_row(p, it, it.row0 + 32 * wave + r);
     bf16x8v q[KS];
@@ -883,186 +869,191 @@ void mx_attn_tile(AttnArgs p)
     lo_least = uniform(lo_least);
     hi_most = uniform(hi_most);
 
-    const int *table = p.table + it.seq * p.table_stride;
-    const bool loads = G::ALL || tid < G::KPL * G::CH;
-    const int mykey = tid / G::CH, chunk = tid % G::CH;
-    v16f o[DT];
+    v16f o[DT], x[2];
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             o[d][i] = 0.0f;
     float m = -__builtin_inff(), l = 0.0f;
+    bf16x8v pb[4];
 
-    AttnTileRegs<G> cur;
-    int page[G::NL];
-    auto pages_of = [&](int key) {
+    // the loaded tile: this thread's chunks, and the keys that are there
+    u4v codes[NI];
+    unsigned scale[NI];
+    unsigned long long loaded = 0;
+    // the keys of the tiles AHEAD .. 0 in front of the softmax that are there
+    unsigned long long there[AHEAD + 1];
+    const bool loads = EVERY || tid < 2 * SIDE;
+    auto load = [&](int t) {
+        const int key = it.key0 + t * BN;
+        loaded = __ballot(page >= 0);
 #pragma unroll
-        for (int j = 0; j < G::NL; ++j)
-            page[j] = loads ? attn_page(p, table, key + mykey + j * G::KPL, it.key1) : -1;
+        for (int i = 0; i < NI; ++i) {
+            const int n = tid + i * THR, side = uniform(n / SIDE), c = n % SIDE, kk = c / G::CH, chunk = c % G::CH;
+            const long long at = attn_row_at(p, __shfl(page, kk), it.head, key + kk);
+            if (loads) {
+                codes[i] = *reinterpret_cast<const u4v *>((side ? p.codes[1] : p.codes[0]) + at * G::RB + 16 * chunk);
+                scale[i] = (side ? p.scales[1] : p.scales[0])[at * G::SB + chunk * G::VC / 32];
+            }
+        }
+        page = attn_page(p, table, key + BN + lane, it.key1);
     };
-    auto load = [&](int key) { attn_load<G>(p, it.head, key + mykey, chunk, page, cur); };
-    auto store_values = [&](char *buf, int j, const u4v &codes, unsigned scale, bool ok, int mode) {
-        u4v w[NP];
-        attn_expand<F>(codes, scale, w);
-        char *at = buf + KBYTES + (mykey + j * G::KPL) * VROW + chunk * G::VC * 2;
-#pragma unroll
-        for (int e = 0; e < NP; ++e)
-            *reinterpret_cast<u4v *>(at + 16 * e) = values_mode(w[e], ok, mode);
-    };
-    // the loaded tile into buffer b
-    auto expand = [&](int b) {
-        char *buf = lds + b * BUF;
-        bool gone = false, nan = false;
+    // the loaded tile t into its buffers
+    auto expand = [&](int t) {
+        const int key = it.key0 + t * BN;
+        char *kbuf = lds + (KBUFS == 1 ? 0 : t % KBUFS) * KBYTES, *vbuf = lds + KBUFS * KBYTES + (t % VBUFS) * VBYTES;
+        const bool whole = loaded == ~0ull && key >= it.all_lo && key + BN <= it.all_hi;
+        bool nan = false;
         if (loads) {
 #pragma unroll
-            for (int j = 0; j < G::NL; ++j) {
-                const int kk = mykey + j * G::KPL;
-                gone |= !cur.ok[j];
-                nan |= attn_has_nan<F>(cur.v[j], cur.vs[j]) && cur.ok[j];
+            for (int i = 0; i < NI; ++i) {
+                const int n = tid + i * THR, side = uniform(n / SIDE), c = n % SIDE, kk = c / G::CH, chunk = c % G::CH;
                 u4v w[NP];
-                attn_expand<F>(cur.k[j], cur.ks[j], w);
+                attn_expand<F>(codes[i], scale[i], w);
+                if (side == 0) {
 #pragma unroll
-                for (int e = 0; e < NP; ++e) {
-                    const int piece = chunk * NP + e;
-                    *reinterpret_cast<u4v *>(buf + ((kk >> 5) * KS + (piece >> 1)) * FS + (piece & 1) * 512 + (kk & 31) * 16) = w[e];
+                    for (int e = 0; e < NP; ++e) {
+                        const int piece = chunk * NP + e;
+                        *reinterpret_cast<u4v *>(kbuf + ((kk >> 5) * KS + (piece >> 1)) * FS + (piece & 1) * 512 + (kk & 31) * 16) = w[e];
+                    }
+                } else {
+                    if (!whole)
+                        nan |= attn_clean(w, loaded >> kk & 1);
+#pragma unroll
+                    for (int e = 0; e < NP; ++e)
+                        *reinterpret_cast<u4v *>(vbuf + kk * VROW + chunk * G::VC * 2 + 16 * e) = w[e];
                 }
-                store_values(buf, j, cur.v[j], cur.vs[j], cur.ok[j], VALUES_PLAIN);
-                if (chunk == 0)
-                    there[b][kk] = cur.ok[j];
             }
         }
-        const unsigned fl = (__any(gone) ? 1u : 0u) | (__any(nan) ? 2u : 0u);
-        if (lane == 0)
-            flags[b][wave] = fl;
+        if (!whole) {
+            const unsigned some = __any(nan);
+            if (lane == 0)
+                nans[t % VBUFS][wave] = some;
+        }
+    };
+    auto sees = [&](int t) {
+        const int key = it.key0 + t * BN;
+        return t >= 0 && t < T && key < hi_most && key + BN > lo_least;
     };
     const int vread = (4 * h + ((r & 15) >> 2)) * VROW + 32 * (r >> 4) + 8 * (r & 3);
-    // values of keys 16 s + 4h .. and 16 s + 8 + 4h .., columns 32 d + r
-    auto values_at = [&](const char *buf, int d, int s) {
-        const char *at = buf + KBYTES + vread + 16 * s * VROW + 64 * d;
-        const u2v a = lds_read_tr(at), b = lds_read_tr(at + 8 * VROW);
-        return as_bf16x8(u4v{a.x, a.y, b.x, b.y});
-    };
 
-    int key = it.key0;
-    if (key < it.key1) {
-        pages_of(key);
-        load(key);
-        pages_of(key + BN);
-        expand(0);
-        if (key + BN < it.key1) {
-            load(key + BN);
-            pages_of(key + 2 * BN);
-        }
-    }
-    block_barrier();
-    for (int b = 0; key < it.key1; key += BN, b ^= 1) {
-        if (key + BN < it.key1) {
-            expand(b ^ 1);
-            if (key + 2 * BN < it.key1) {
-                load(key + 2 * BN);
-                pages_of(key + 3 * BN);
+    auto phase_m = [&](int t) {
+        if (sees(t - 1)) {
+            const int key = it.key0 + (t - 1) * BN;
+            const char *buf = lds + KBUFS * KBYTES + ((t - 1) % VBUFS) * VBYTES + vread;
+            // values of keys 16 s + 4h .. and 16 s + 8 + 4h .., columns 32 d + r
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const char *at = buf + 16 * s * VROW + 64 * d;
+                    const u2v a = lds_read_tr(at), b = lds_read_tr(at + 8 * VROW);
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(u4v{a.x, a.y, b.x, b.y}), pb[s], o[d], 0, 0, 0);
+                }
+            if (!(there[0] == ~0ull && key >= it.all_lo && key + BN <= it.all_hi)) {
+                unsigned some = 0;
+#pragma unroll
+                for (int w = 0; w < NW; ++w)
+                    some |= nans[(t - 1) % VBUFS][w];
+                if (uniform(some))
+                    attn_poison<F, D, DT * 4>(p, table, it, key, BN, row, [&](int j, auto &&put) {
+                        v16f &s = o[j >> 2];
+                        const int i = 4 * (j & 3);
+                        float a = s[i], b = s[i + 1], c = s[i + 2], e = s[i + 3];
+                        put(32 * (j >> 2) + 8 * (j & 3) + 4 * h, a, b, c, e);
+                        s[i] = a;
+                        s[i + 1] = b;
+                        s[i + 2] = c;
+                        s[i + 3] = e;
+                    });
             }
         }
-        char *buf = lds + b * BUF;
-        const unsigned fl = flags[b][0] | flags[b][1] | flags[b][2] | flags[b][3];
-        // (uniform over the workgroup: the values are rewritten below)
-        const bool careful = (uniform(fl) & 2) && !(key >= it.all_lo && key + BN <= it.all_hi && !(uniform(fl) & 1));
-        if (careful) {
-#pragma unroll
-            for (int j = 0; j < G::NL; ++j)
-                if (loads) {
-                    const int k = key + mykey + j * G::KPL, pg = attn_page(p, table, k, it.key1);
-                    const long long at = attn_row_at(p, pg, it.head, k);
-                    store_values(buf, j, *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + 16 * chunk),
-                                 p.scales[1][at * G::SB + chunk * G::VC / 32], pg >= 0, VALUES_CLEAN);
-                }
-            block_barrier();
-        }
-        unsigned vis = 0xFFFFFFFFu;         // bit 16 kt + i: the row sees key 32 kt + 8 (i >> 2) + 4h + (i & 3)
-        if (key < hi_most && key + BN > lo_least) {
-            v16f x[2];
+        if (sees(t)) {
+            const char *buf = lds + (KBUFS == 1 ? 0 : t % KBUFS) * KBYTES + lane * 16;
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
                 for (int kt = 0; kt < 2; ++kt) {
-                    const bf16x8v f = as_bf16x8(*reinterpret_cast<const u4v *>(buf + (kt * KS + s) * FS + lane * 16));
+                    const bf16x8v f = as_bf16x8(*reinterpret_cast<const u4v *>(buf + (kt * KS + s) * FS));
                     if (s == 0)
                         x[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[s], v16f{}, 0, 0, 0);
                     else
                         x[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[s], x[kt], 0, 0, 0);
                 }
-            if (!(key >= lo_most && key + BN <= hi_least && !(uniform(fl) & 1))) {
-                vis = 0;
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int kk = 32 * (e >> 4) + 8 * ((e & 15) >> 2) + 4 * h + (e & 3), k = key + kk;
-                    const bool see = k >= row.lo && k < row.hi && there[b][kk];
-                    vis |= (unsigned)see << e;
-                    x[e >> 4][e & 15] = see ? x[e >> 4][e & 15] : -__builtin_inff();
-                }
-            }
-            float top = -__builtin_inff();
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                top = fmaxf(top, x[e >> 4][e & 15]);
-            top = fmaxf(top, __shfl_xor(top, 32)) * p.c;
-            if (__any(top > m + kRescale)) {
-                const float mn = fmaxf(m, top);
-                const float w = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-                l *= w;
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[d][i] *= w;
-                m = mn;
-            }
-            const float ref = m == -__builtin_inff() ? 0.0f : m;
-            bf16x8v pb[4];
+        }
+    };
+    auto softmax = [&](int t) {
+        const int key = it.key0 + t * BN;
+        if (!(there[0] == ~0ull && key >= lo_most && key + BN <= hi_least)) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-                const float w = __builtin_amdgcn_exp2f(fmaf(x[e >> 4][e & 15], p.c, -ref));
-                l += w;
-                pb[e >> 3][e & 7] = (__bf16)w;
+                const int kk = 32 * (e >> 4) + 8 * ((e & 15) >> 2) + 4 * h + (e & 3), k = key + kk;
+                const bool see = k >= row.lo && k < row.hi && (there[0] >> kk & 1);
+                x[e >> 4][e & 15] = see ? x[e >> 4][e & 15] : -__builtin_inff();
             }
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_at(buf, d, s), pb[s], o[d], 0, 0, 0);
-        } else {
-            vis = 0;
         }
-        if (careful) {
-            // ones where the values are NaN; a row that sees one gets a NaN there
-            block_barrier();
+        float top = -__builtin_inff();
 #pragma unroll
-            for (int j = 0; j < G::NL; ++j)
-                if (loads) {
-                    const int k = key + mykey + j * G::KPL, pg = attn_page(p, table, k, it.key1);
-                    const long long at = attn_row_at(p, pg, it.head, k);
-                    store_values(buf, j, *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + 16 * chunk),
-                                 p.scales[1][at * G::SB + chunk * G::VC / 32], pg >= 0, VALUES_NAN);
-                }
-            block_barrier();
-            bf16x8v seen[4];
+        for (int e = 0; e < 32; ++e)
+            top = fmaxf(top, x[e >> 4][e & 15]);
+        top = max_across_32(top) * p.c;
+        if (__any(top > m + kRescale)) {
+            const float mn = fmaxf(m, top);
+            const float w = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+            l *= w;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-                seen[e >> 3][e & 7] = (vis >> e & 1) ? (__bf16)1.0f : (__bf16)0.0f;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                v16f bad = {};
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    bad = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values_at(buf, d, s), seen[s], bad, 0, 0, 0);
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    o[d][i] = bad[i] > 0.0f ? __builtin_nanf("") : o[d][i];
+                    o[d][i] *= w;
+            m = mn;
+        }
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const float w = __builtin_amdgcn_exp2f(fmaf(x[e >> 4][e & 15], p.c, -ref));
+            l += w;
+            pb[e >> 3][e & 7] = (__bf16)w;
+        }
+    };
+
+    if (T > 0) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            there[a + 1] = 0;
+            if (a < T) {
+                load(a);
+                expand(a);
+                there[a + 1] = loaded;
             }
         }
+        if (AHEAD < T)
+            load(AHEAD);
         block_barrier();
+        if (NW == 8 && wave >= 4)
+            block_barrier();
+        for (int t = 0; t < T; ++t) {
+            phase_m(t);
+            block_barrier();
+#pragma unroll
+            for (int a = 0; a < AHEAD; ++a)
+                there[a] = there[a + 1];
+            if (sees(t))
+                softmax(t);
+            if (t + AHEAD < T) {
+                expand(t + AHEAD);
+                there[AHEAD] = loaded;
+                if (t + AHEAD + 1 < T)
+                    load(t + AHEAD + 1);
+            }
+            block_barrier();
+        }
+        phase_m(T);
+        if (NW == 8 && wave < 4)
+            block_barrier();
     }
+    __syncthreads();
 
     l += __shfl_xor(l, 32);
     if (h == 0) {
@@ -1076,9 +1067,9 @@ void mx_attn_tile(AttnArgs p)
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<v4f *>(mine + 32 * d + 8 * i) = v4f{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
     __syncthreads();
-    attn_finish<D, BM, 256>(p, it, tid, [&](int u, float (&f)[8], float &mm, float &ll) {
+    attn_finish<D, BM, THR>(p, it, tid, [&](int u, float (&f)[8], float &mm, float &ll) {
         constexpr int RUNS = D / 8;
-        const int i = tid + 256 * u, n = i / RUNS;
+        const int i = tid + THR * u, n = i / RUNS;
         const float *src = reinterpret_cast<const float *>(lds) + n * OROW + i % RUNS * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e)

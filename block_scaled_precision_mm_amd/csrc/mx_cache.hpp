@@ -80,7 +80,9 @@ void mx_cache_write(CacheArgs p)
 // Eight values of a block with E8M0 code s, as BF16 pairs: element times
 // 2^(s - 127), rounded to nearest even where a BF16 cannot hold it (blocks
 // of subnormal BF16 values only); NaN for s = 255 and for E4M3 NaN codes.
-// The conversions take s as an exponent field, 0 included.
+// The conversions take s as an exponent field, 0 included, and give NaN for
+// every code under the field 255 (checked on MI355X for all codes under all
+// scales).
 template <int F>
 __device__ __forceinline__ u4v mx_decode8(u2v c, unsigned s)
 {
@@ -97,8 +99,6 @@ __device__ __forceinline__ u4v mx_decode8(u2v c, unsigned s)
         w[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], sc, false));
         w[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[1], sc, true));
     }
-    if (s == 255u)
-        w = u4v{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
     return w;
 }
 

@@ -170,32 +170,36 @@ int run_cache(bool write, const mxg_kv_cache_t *c, const void *k, const void *v,
 // ----------------------------------------------------------------- attention
 typedef void (*AttnFn)(AttnArgs);
 
-// One kernel of the launch: rows per tile, workgroups that can run at once.
-struct AttnKernel {
-    AttnFn fn;
-    int bm, target;
-};
+// Row tiles of 16 or 32 rows in mx_attn_rows, of 128 or 256 in mx_attn_tile.
+enum { ROWS_16 = 0, ROWS_32 = 1, ROWS_128 = 2, ROWS_256 = 3 };
+constexpr int kAttnBM[4] = {16, 32, 128, 256};
+constexpr int kAttnThreads[4] = {256, 256, 256, 512};
+// workgroups that run at once on 256 CUs
+constexpr int kAttnTarget[4] = {768, 512, 512, 256};
 
-// Row tiles of 16 (32) rows in mx_attn_rows, of 128 in mx_attn_tile.
-enum { ROWS_16 = 0, ROWS_32 = 1, ROWS_128 = 2 };
-constexpr int kAttnBM[3] = {16, 32, 128};
-
-template <int F, int D>
+template <int F, int D, int PAGED>
 AttnFn attn_fn(int which)
 {
-    return which == ROWS_16 ? &mx_attn_rows<F, D, 1> : which == ROWS_32 ? &mx_attn_rows<F, D, 2> : &mx_attn_tile<F, D>;
+    switch (which) {
+    case ROWS_16: return &mx_attn_rows<F, D, 1, PAGED>;
+    case ROWS_32: return &mx_attn_rows<F, D, 2, PAGED>;
+    case ROWS_128: return &mx_attn_tile<F, D, 4>;
+    default: return &mx_attn_tile<F, D, 8>;
+    }
 }
 
-AttnKernel attn_kernel(int which, bool fp4, int dim)
+template <int F, int D>
+AttnFn attn_fn(int which, int64_t page_size)
 {
-    AttnKernel k;
-    k.bm = kAttnBM[which];
-    k.target = which == ROWS_16 ? 1024 : 512;
+    // a load instruction of mx_attn_rows covers 64 chunks of 16 bytes
+    return page_size >= 64 / AttnGeom<F, D>::CH ? attn_fn<F, D, 1>(which) : attn_fn<F, D, 0>(which);
+}
+
+AttnFn attn_fn(int which, bool fp4, int64_t dim, int64_t page_size)
+{
     if (dim == 64)
-        k.fn = fp4 ? attn_fn<FMT_FP4, 64>(which) : attn_fn<FMT_FP8, 64>(which);
-    else
-        k.fn = fp4 ? attn_fn<FMT_FP4, 128>(which) : attn_fn<FMT_FP8, 128>(which);
-    return k;
+        return fp4 ? attn_fn<FMT_FP4, 64>(which, page_size) : attn_fn<FMT_FP8, 64>(which, page_size);
+    return fp4 ? attn_fn<FMT_FP4, 128>(which, page_size) : attn_fn<FMT_FP8, 128>(which, page_size);
 }
 
 // What a call launches: one kernel for all sequences, or one for those of
@@ -212,14 +216,15 @@ AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
 {
     AttnPlan p = {};
     const int64_t most = max_new * group;       // rows of the longest
-    if (most <= 16 || most <= 32 || tokens == seqs * max_new) {
+    const int tile = most > 128 ? ROWS_256 : ROWS_128;
+    if (most <= 32 || tokens == seqs * max_new) {
         p.n = 1;
-        p.which[0] = most <= 16 ? ROWS_16 : most <= 32 ? ROWS_32 : ROWS_128;
+        p.which[0] = most <= 16 ? ROWS_16 : most <= 32 ? ROWS_32 : tile;
         p.above[0] = 0;
         p.upto[0] = INT32_MAX;
     } else {
         p.n = 2;
-        p.which[0] = ROWS_128;
+        p.which[0] = tile;
         p.above[0] = 32;
         p.upto[0] = INT32_MAX;
         p.which[1] = ROWS_32;
@@ -227,11 +232,10 @@ AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
         p.upto[1] = 32;
     }
     for (int i = 0; i < p.n; ++i) {
-        const int bm = kAttnBM[p.which[i]];
-        const AttnKernel k = attn_kernel(p.which[i], false, (int)dim);
+        const int bm = kAttnBM[p.which[i]], target = kAttnTarget[p.which[i]];
         const int64_t some = std::min(seqs, tokens);        // sequences with a new token
         p.base[i] = heads * (p.upto[i] <= bm ? some : tokens * group / bm + some);
-        p.bytes[i] = p.base[i] <= kSplitCounters ? (size_t)2 * k.target * attn_slot_bytes(bm, (int)dim) : 0;
+        p.bytes[i] = p.base[i] <= kSplitCounters ? (size_t)2 * target * attn_slot_bytes(bm, (int)dim) : 0;
     }
     return p;
 }
@@ -330,6 +334,8 @@ int mx_paged_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_str
     a.tokens = (int)tokens;
     a.heads = (int)cache->kv_heads;
     a.group = (int)group;
+    a.by_heads = fast_div((unsigned)a.heads);
+    a.by_group = fast_div((unsigned)a.group);
     a.page_shift = log2_of(cache->page_size);
     a.pages = (int)cache->pages;
     a.table_width = (int)table_width;
@@ -337,17 +343,18 @@ int mx_paged_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_str
     a.window = (int)std::min<int64_t>(window, 1 << 30);
     a.out_kind = out_dtype;
     for (int i = 0; i < plan.n; ++i) {
-        const AttnKernel k = attn_kernel(plan.which[i], cache->is_fp4 != 0, (int)cache->head_dim);
+        const int which = plan.which[i];
         const bool parts = split && plan.bytes[i] > 0;
         a.counters = parts ? (unsigned *)workspace : nullptr;
         a.parts = parts ? (uint8_t *)workspace + kSplitCounters * sizeof(unsigned) : nullptr;
         a.rows_above = plan.above[i];
         a.rows_upto = plan.upto[i];
-        a.target = k.target;
-        const int64_t grid = plan.base[i] + (parts ? k.target : 0);
+        a.per_target = (float)a.heads / (float)kAttnTarget[which];
+        const int64_t grid = plan.base[i] + (parts ? kAttnTarget[which] : 0);
         if (grid > INT32_MAX)
             return MXG_ERR_SHAPE;
-        hipLaunchKernelGGL(k.fn, dim3((unsigned)grid), dim3(256), 0, (hipStream_t)stream, a);
+        hipLaunchKernelGGL(attn_fn(which, cache->is_fp4 != 0, cache->head_dim, cache->page_size), dim3((unsigned)grid),
+                           dim3(kAttnThreads[which]), 0, (hipStream_t)stream, a);
         rc = host_hip_status(hipGetLastError());
         if (rc)
             return rc;
