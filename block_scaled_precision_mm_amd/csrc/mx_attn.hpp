@@ -57,6 +57,18 @@
 namespace mxg {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
+
+// Compile-time loop: f(IntC<B>) for B in [B0, B1).
+template <int N> struct IntC { static constexpr int value = N; };
+template <int B0, int B1, class Fn>
+__device__ __forceinline__ void static_range(Fn &&f)
+{
+    if constexpr (B0 < B1) {
+        f(IntC<B0>{});
+        static_range<B0 + 1, B1>(f);
+    }
+}
+
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 typedef short s16x4v __attribute__((ext_vector_type(4)));
 
@@ -262,6 +274,14 @@ __device__ __forceinline__ AttnRow attn_row(const AttnArgs &p, const AttnItem &i
     return r;
 }
 
+// Bits [lo, hi) of 64.
+__device__ __forceinline__ unsigned long long bit_range(int lo, int hi)
+{
+    const unsigned long long from = lo <= 0 ? ~0ull : lo >= 64 ? 0ull : ~0ull << lo;
+    const unsigned long long upto = hi >= 64 ? ~0ull : hi <= 0 ? 0ull : ~(~0ull << hi);
+    return from & upto;
+}
+
 // Rows of codes and scales, and the 16-byte chunks of a row.
 template <int F, int D>
 struct AttnGeom {
@@ -280,6 +300,19 @@ __device__ __forceinline__ int attn_page(const AttnArgs &p, const int *table, in
     if (key < key1)
         page = table[key >> p.page_shift];
     return (unsigned)page < (unsigned)p.pages ? page : -1;
+}
+
+// The same in two steps, the table's entry loaded ahead (that of the last key
+// past key1; key1 > 0) and looked at when it is needed: a comparison right
+// behind the load would wait for it.
+__device__ __forceinline__ int attn_entry(const AttnArgs &p, const int *table, int key, int key1)
+{
+    return table[min(key, key1 - 1) >> p.page_shift];
+}
+
+__device__ __forceinline__ int attn_page_of(const AttnArgs &p, int entry, int key, int key1)
+{
+    return key < key1 && (unsigned)entry < (unsigned)p.pages ? entry : -1;
 }
 
 // Row of the cache (codes and scales) of key `key` on page `page`.  A key
@@ -339,29 +372,28 @@ __device__ __forceinline__ unsigned attn_nan4(const AttnArgs &p, long long at, i
     return m;
 }
 
-// The rows of this lane that see a key with NaNs among its values get them.
-// keys [key, key + n) of a tile whose NaNs became zeros; group(j, f) calls
-// f(d, v) for its j-th run of four sums v at columns d .. d + 3.
-template <int F, int D, int NG, class Group>
-__device__ __forceinline__ void attn_poison(const AttnArgs &p, const int *table, const AttnItem &it, int key, int n,
-                                            const AttnRow &row, Group &&group)
+// The sums of this lane's row that see a NaN among the values of keys
+// [key, key + n) of a tile whose NaNs became zeros: bit 4 j + i for value
+// column(j) + i.  (As bits that are looked at after the last tile: written
+// into the sums here, in a branch, they would be copied in every tile.)
+template <int F, int D, int NG, class Column>
+__device__ __forceinline__ unsigned long long attn_poison(const AttnArgs &p, const int *table, const AttnItem &it, int key,
+                                                          int n, const AttnRow &row, Column &&column)
 {
+    static_assert(NG <= 16, "bits");
+    unsigned long long bits = 0;
     for (int k = key; k < min(key + n, it.key1); ++k) {
         const int page = attn_page(p, table, k, it.key1);
         if (page < 0)
             continue;
         const long long at = attn_row_at(p, page, it.head, k);
         const bool see = k >= row.lo && k < row.hi;
-#pragma unroll
-        for (int j = 0; j < NG; ++j)
-            group(j, [&](int d, float &a, float &b, float &c, float &e) {
-                const unsigned m = see ? attn_nan4<F, D>(p, at, d) : 0u;
-                a = m & 1 ? __builtin_nanf("") : a;
-                b = m & 2 ? __builtin_nanf("") : b;
-                c = m & 4 ? __builtin_nanf("") : c;
-                e = m & 8 ? __builtin_nanf("") : e;
-            });
+        for (int j = 0; j < NG; ++j) {
+            const unsigned m = see ? attn_nan4<F, D>(p, at, column(j)) : 0u;
+            bits |= (unsigned long long)m << (4 * j);
+        }
     }
+    return bits;
 }
 
 __device__ __forceinline__ bf16x8v as_bf16x8(u4v v) { return __builtin_bit_cast(bf16x8v, v); }
@@ -567,7 +599,8 @@ void mx_attn_rows(AttnArgs p)
     const int *table = p.table + it.seq * p.table_stride;
     const int mykey = lane / G::CH, chunk = lane % G::CH;
     int key = it.key0 + wave * KT;
-    int page = attn_page(p, table, key + (lane & 31), it.key1);     // of key `lane & 31` of the next tile loaded
+    // table entry of key `lane & 31` of the next tile loaded
+    int entry = it.key0 < it.key1 ? attn_entry(p, table, key + (lane & 31), it.key1) : -1;
 
     AttnRow row[QT];
     bf16x8v q[QT][KS];
@@ -584,6 +617,7 @@ void mx_attn_rows(AttnArgs p)
     char *mem = lds + wave * WBYTES;
     v4f o[QT][DT];
     float m[QT], l[QT];
+    unsigned long long poison[QT] = {};
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         m[t] = -__builtin_inff();
@@ -599,6 +633,7 @@ void mx_attn_rows(AttnArgs p)
     unsigned ks[NL], vs[NL], there = 0;
     const unsigned voff = mykey * G::RB + chunk * 16, soff = mykey * G::SB + chunk * G::VC / 32;
     auto load = [&](int k) {
+        const int page = attn_page_of(p, entry, k + (lane & 31), it.key1);
         there = (unsigned)__ballot(page >= 0);
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
@@ -617,7 +652,7 @@ void mx_attn_rows(AttnArgs p)
                 vs[j] = p.scales[1][at * G::SB + chunk * G::VC / 32];
             }
         }
-        page = attn_page(p, table, k + BN + (lane & 31), it.key1);
+        entry = attn_entry(p, table, k + BN + (lane & 31), it.key1);
     };
     auto wave_fence = [] {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -665,18 +700,18 @@ void mx_attn_rows(AttnArgs p)
             for (int e = 0; e < NP; ++e)
                 *reinterpret_cast<u4v *>(vput + j * KPL * VROW + 16 * e) = w[e];
         }
-        if (key + BN < it.key1)
-            load(key + BN);
+        // (past the last key: row 0 of the cache, not used.  Under a condition
+        // the loop would wait for the loads it has just issued, to merge them
+        // with the registers' old contents)
+        load(key + BN);
         bf16x8v pb[QT];
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             if (!whole) {
+                const unsigned see = (unsigned)bit_range(row[t].lo - key, row[t].hi - key) & here;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int kk = 16 * (e >> 2) + 4 * g + (e & 3), k = key + kk;
-                    const bool see = k >= row[t].lo && k < row[t].hi && (here >> kk & 1);
-                    x[t][e >> 2][e & 3] = see ? x[t][e >> 2][e & 3] : -__builtin_inff();
-                }
+                for (int e = 0; e < 8; ++e)
+                    x[t][e >> 2][e & 3] = see >> (4 * g) >> (16 * (e >> 2) + (e & 3)) & 1 ? x[t][e >> 2][e & 3] : -__builtin_inff();
             }
             float top = -__builtin_inff();
 #pragma unroll
@@ -714,16 +749,20 @@ void mx_attn_rows(AttnArgs p)
                 o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, pb[t], o[t][d], 0, 0, 0);
         }
         wave_fence();
-        if (!whole && __any(nan)) {
+        if (__builtin_expect(!whole && __any(nan), 0)) {
 #pragma unroll
             for (int t = 0; t < QT; ++t)
-                attn_poison<F, D, DT>(p, table, it, key, KT, row[t], [&](int d, auto &&put) {
-                    float a = o[t][d][0], b = o[t][d][1], c = o[t][d][2], e = o[t][d][3];
-                    put(16 * d + 4 * g, a, b, c, e);
-                    o[t][d] = v4f{a, b, c, e};
-                });
+                poison[t] |= attn_poison<F, D, DT>(p, table, it, key, KT, row[t], [&](int j) { return 16 * j + 4 * g; });
         }
     }
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+        if (__builtin_expect(__any(poison[t] != 0), 0))
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[t][d][i] = poison[t] >> (4 * d + i) & 1 ? __builtin_nanf("") : o[t][d][i];
 
     // join the four waves, 16 rows at a time
 #pragma unroll
@@ -793,6 +832,15 @@ void mx_attn_rows(AttnArgs p)
 }
 
 // ------------------------------------------------------------ many rows
+// Slot permutation of a key's row of values in LDS: slot p (16 bytes) of the
+// row lies at p ^ value_swizzle.  A row of 128 values is the 256 bytes of all
+// banks, one of 64 values half of them.
+template <int D>
+__device__ __forceinline__ int value_swizzle(int key)
+{
+    return D >= 128 ? (key & 3) * 5 : (key >> 1 & 1) * 4 + (key >> 1 & 3);
+}
+
 // Row tiles of 32 NW rows, 32 per wave, over tiles of 64 keys that the waves
 // expand together.  A wave alternates between two phases with a barrier after
 // each:
@@ -813,11 +861,15 @@ void mx_attn_rows(AttnArgs p)
 // 16s + 8 + 4h + i of the tile.
 //
 // LDS of a buffer: the keys as operand fragments (lane order, 1 KB each,
-// apart by 1 KB + 128 bytes so that the expanding stores of a key's steps
-// fall on different banks), or the values as rows of 2D + 64 bytes (the
-// four keys and two column groups of a half's transposing read then cover
-// the banks once).
-template <int F, int D, int NW>
+// apart by 1 KB + 4096 / D bytes), or the values as rows of 2D bytes whose
+// 16-byte slots are permuted by the key (value_swizzle).  Both so that 16
+// lanes of an expanding store (the chunks of a few keys) and 32 lanes of a
+// transposing read (four keys, 64 bytes of each) touch every bank once: with
+// rows and fragments padded by 64 and 128 bytes the LDS spent 1000 of 2400
+// busy cycles per tile on conflicts.
+//
+// PAGED as in mx_attn_rows.
+template <int F, int D, int NW, int PAGED>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void mx_attn_tile(AttnArgs p)
 {
@@ -825,13 +877,15 @@ void mx_attn_tile(AttnArgs p)
     using G = AttnGeom<F, D>;
     constexpr int KS = D / 16, DT = D / 32, NP = G::NP;
     constexpr int AHEAD = NW == 8 ? 2 : 1, KBUFS = NW == 8 ? 3 : 1, VBUFS = NW == 8 ? 4 : 2;
-    constexpr int FS = 1024 + 128, KBYTES = 2 * KS * FS, VROW = 2 * D + 64, VBYTES = BN * VROW;
+    constexpr int FS = 1024 + 4096 / D, KBYTES = 2 * KS * FS, VROW = 2 * D, VBYTES = BN * VROW;
     constexpr int OROW = D + 4;
     constexpr int TILES = KBUFS * KBYTES + VBUFS * VBYTES;
     constexpr int BYTES = TILES > BM * OROW * 4 ? TILES : BM * OROW * 4;
-    // chunk n of the 2 x 64 CH of a tile (keys, then values): thread n % THR
-    constexpr int SIDE = BN * G::CH, NI = cdiv_c(2 * SIDE, THR);
-    constexpr bool EVERY = 2 * SIDE >= THR;
+    // chunk n of the 2 x 64 CH of a tile (keys, then values): thread n % THR.
+    // A wave's chunks are of one side (with SIDE >= THR known at compile time)
+    // and of KPW consecutive keys from wave * KPW + i * THR / CH on.
+    constexpr int SIDE = BN * G::CH, NI = cdiv_c(2 * SIDE, THR), KPW = 64 / G::CH;
+    constexpr bool EVERY = 2 * SIDE >= THR, STATIC = SIDE >= THR;
     __shared__ __attribute__((aligned(1024))) char lds[BYTES];
     __shared__ float ml[BM][2];
     __shared__ unsigned nans[VBUFS][NW];                // a NaN became a zero in the tile (by wave)
@@ -843,7 +897,9 @@ void mx_attn_tile(AttnArgs p)
 
     const int *table = p.table + it.seq * p.table_stride;
     const int T = (it.key1 - it.key0 + BN - 1) / BN;
-    int page = attn_page(p, table, it.key0 + lane, it.key1);        // of key `lane` of the next tile loaded
+    // table entry of key `lane` of the next tile loaded
+    int entry = T > 0 ? attn_entry(p, table, it.key0 + lane, it.key1) : -1;
+    const int chunk = tid % G::CH;                                  // THR is a multiple of CH
 
     const AttnRow row = attn_row(p, it, it.row0 + 32 * wave + r);
     bf16x8v q[KS];
@@ -876,7 +932,11 @@ void mx_attn_tile(AttnArgs p)
         for (int i = 0; i < 16; ++i)
             o[d][i] = 0.0f;
     float m = -__builtin_inff(), l = 0.0f;
+    unsigned long long poison = 0;
     bf16x8v pb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
 
     // the loaded tile: this thread's chunks, and the keys that are there
     u4v codes[NI];
@@ -884,113 +944,168 @@ void mx_attn_tile(AttnArgs p)
     unsigned long long loaded = 0;
     // the keys of the tiles AHEAD .. 0 in front of the softmax that are there
     unsigned long long there[AHEAD + 1];
+    // (threads without a chunk load an earlier one's and do not expand it)
     const bool loads = EVERY || tid < 2 * SIDE;
+    const int myside = STATIC ? 0 : uniform(wave * 64 / SIDE);
+    auto side_of = [&](int i) { return STATIC ? i * THR / SIDE : myside & 1; };
+    auto key_of = [&](int i) { return STATIC ? wave * KPW + i * THR % SIDE / G::CH : (wave * KPW) & (BN - 1); };
+    const int mykey = lane / G::CH;
+    // rows of the cache per page, and of the pages before this head's
+    const int page_rows = p.heads << p.page_shift, head_row = it.head << p.page_shift, in_page = (1 << p.page_shift) - 1;
+    const unsigned voff = mykey * G::RB + 16 * chunk, soff = mykey * G::SB + chunk * G::VC / 32;
     auto load = [&](int t) {
         const int key = it.key0 + t * BN;
+        const int page = attn_page_of(p, entry, key + lane, it.key1);
         loaded = __ballot(page >= 0);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int n = tid + i * THR, side = uniform(n / SIDE), c = n % SIDE, kk = c / G::CH, chunk = c % G::CH;
-            const long long at = attn_row_at(p, __shfl(page, kk), it.head, key + kk);
-            if (loads) {
-                codes[i] = *reinterpret_cast<const u4v *>((side ? p.codes[1] : p.codes[0]) + at * G::RB + 16 * chunk);
-                scale[i] = (side ? p.scales[1] : p.scales[0])[at * G::SB + chunk * G::VC / 32];
+            const uint8_t *cp = side_of(i) ? p.codes[1] : p.codes[0], *sp = side_of(i) ? p.scales[1] : p.scales[0];
+            const int k0 = key_of(i);
+            if constexpr (PAGED) {
+                // the row of the wave's first key is a scalar (a key that is
+                // not there: of page 0, in bounds and not used)
+                const unsigned long long at = (unsigned long long)(unsigned)max(lane_value(page, k0), 0) * (unsigned)page_rows +
+                                              (unsigned)(head_row + ((key + k0) & in_page));
+                codes[i] = *reinterpret_cast<const u4v *>(cp + at * G::RB + voff);
+                scale[i] = (sp + at * G::SB)[soff];
+            } else {
+                const long long at = attn_row_at(p, __shfl(page, k0 + mykey), it.head, key + k0 + mykey);
+                codes[i] = *reinterpret_cast<const u4v *>(cp + at * G::RB + 16 * chunk);
+                scale[i] = sp[at * G::SB + chunk * G::VC / 32];
             }
         }
-        page = attn_page(p, table, key + BN + lane, it.key1);
+        entry = attn_entry(p, table, key + BN + lane, it.key1);
+    };
+    // where this thread's chunks go in a buffer of keys and one of values
+    auto put_key = [&](int i, int e) {
+        const int kk = key_of(i) + mykey, piece = chunk * NP + e;
+        return ((kk >> 5) * KS + (piece >> 1)) * FS + (piece & 1) * 512 + (kk & 31) * 16;
+    };
+    auto put_value = [&](int i, int e) {
+        const int kk = key_of(i) + mykey;
+        return kk * VROW + 16 * ((chunk * NP + e) ^ value_swizzle<D>(kk));
     };
     // the loaded tile t into its buffers
     auto expand = [&](int t) {
         const int key = it.key0 + t * BN;
-        char *kbuf = lds + (KBUFS == 1 ? 0 : t % KBUFS) * KBYTES, *vbuf = lds + KBUFS * KBYTES + (t % VBUFS) * VBYTES;
+        char *kbuf = lds + (KBUFS == 1 ? 0 : (unsigned)t % KBUFS) * KBYTES;
+        char *vbuf = lds + KBUFS * KBYTES + (unsigned)t % VBUFS * VBYTES;
         const bool whole = loaded == ~0ull && key >= it.all_lo && key + BN <= it.all_hi;
         bool nan = false;
-        if (loads) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int n = tid + i * THR, side = uniform(n / SIDE), c = n % SIDE, kk = c / G::CH, chunk = c % G::CH;
-                u4v w[NP];
-                attn_expand<F>(codes[i], scale[i], w);
-                if (side == 0) {
-#pragma unroll
-                    for (int e = 0; e < NP; ++e) {
-                        const int piece = chunk * NP + e;
-                        *reinterpret_cast<u4v *>(kbuf + ((kk >> 5) * KS + (piece >> 1)) * FS + (piece & 1) * 512 + (kk & 31) * 16) = w[e];
-                    }
-                } else {
-                    if (!whole)
-                        nan |= attn_clean(w, loaded >> kk & 1);
+        for (int i = 0; i < NI; ++i) {
+            u4v w[NP];
+            attn_expand<F>(codes[i], scale[i], w);
+            if (side_of(i) == 0) {
+                if (loads)
 #pragma unroll
                     for (int e = 0; e < NP; ++e)
-                        *reinterpret_cast<u4v *>(vbuf + kk * VROW + chunk * G::VC * 2 + 16 * e) = w[e];
-                }
+                        *reinterpret_cast<u4v *>(kbuf + put_key(i, e)) = w[e];
+            } else {
+                if (__builtin_expect(!whole, 0))
+                    nan |= attn_clean(w, loaded >> (key_of(i) + mykey) & 1) && loads;
+                if (loads)
+#pragma unroll
+                    for (int e = 0; e < NP; ++e)
+                        *reinterpret_cast<u4v *>(vbuf + put_value(i, e)) = w[e];
             }
         }
-        if (!whole) {
+        if (__builtin_expect(!whole, 0)) {
             const unsigned some = __any(nan);
             if (lane == 0)
-                nans[t % VBUFS][wave] = some;
+                nans[(unsigned)t % VBUFS][wave] = some;
         }
     };
     auto sees = [&](int t) {
         const int key = it.key0 + t * BN;
         return t >= 0 && t < T && key < hi_most && key + BN > lo_least;
     };
-    const int vread = (4 * h + ((r & 15) >> 2)) * VROW + 32 * (r >> 4) + 8 * (r & 3);
+    // this lane's piece of a transposing read: key 4h + (r & 15) / 4 of eight,
+    // 8 bytes r & 3 of the 32 at column group r >> 4 (eight keys on, and 64
+    // bytes on, the permutation is the same but for the 64's own slots)
+    const int vkey = 4 * h + ((r & 15) >> 2);
+    const int vread = vkey * VROW + 8 * (r & 1), vslot = 2 * (r >> 4) + ((r & 3) >> 1);
 
+    // The M phase is eight batches of DT MFMAs with their LDS reads two
+    // batches ahead: 0 .. 3 the second product's steps of 16 keys of tile
+    // t - 1, 4 .. 7 a quarter of the first product of tile t.
+    u4v frag[3][DT];
+    auto fetch = [&](auto bc, int t) {
+        constexpr int b = decltype(bc)::value;
+        if constexpr (b < 4) {
+            // values of keys 16 b + 4h .. and 16 b + 8 + 4h .., columns 32 d + r
+            const char *at = lds + KBUFS * KBYTES + (unsigned)max(t - 1, 0) % VBUFS * VBYTES + vread + 16 * b * VROW;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const char *slot = at + 16 * ((4 * d + vslot) ^ value_swizzle<D>(vkey));
+                const u2v lo = lds_read_tr(slot), hi = lds_read_tr(slot + 8 * VROW);
+                frag[b % 3][d] = u4v{lo.x, lo.y, hi.x, hi.y};
+            }
+        } else {
+            const char *at = lds + (KBUFS == 1 ? 0 : (unsigned)t % KBUFS) * KBYTES + lane * 16;
+#pragma unroll
+            for (int i = 0; i < DT; ++i)
+                frag[b % 3][i] = *reinterpret_cast<const u4v *>(at + ((i & 1) * KS + (b - 4) * (DT / 2) + (i >> 1)) * FS);
+        }
+    };
+    auto multiply = [&](auto bc) {
+        constexpr int b = decltype(bc)::value;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+            const bf16x8v f = as_bf16x8(frag[b % 3][i]);
+            if constexpr (b < 4) {
+                o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[b], o[i], 0, 0, 0);
+            } else {
+                constexpr int s0 = (b - 4) * (DT / 2);
+                if (s0 + (i >> 1) == 0)
+                    x[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[0], v16f{}, 0, 0, 0);
+                else
+                    x[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[s0 + (i >> 1)], x[i & 1], 0, 0, 0);
+            }
+        }
+    };
+    auto batches = [&](auto from, auto upto, int t) {
+        constexpr int B0 = decltype(from)::value, B1 = decltype(upto)::value;
+        fetch(IntC<B0>{}, t);
+        fetch(IntC<B0 + 1>{}, t);
+        __builtin_amdgcn_sched_barrier(0);
+        static_range<B0, B1>([&](auto b) {
+            constexpr int i = decltype(b)::value;
+            if constexpr (i + 2 < B1)
+                fetch(IntC<i + 2>{}, t);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(b);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
     auto phase_m = [&](int t) {
+        // No branches, so that the sums stay in their registers: where a wave
+        // saw nothing of tile t - 1 its p are zeros, and the values finite (a
+        // tile that not every row sees whole holds no NaN); t = 0 takes tile
+        // 0's values for those before it.  Past the last tile the first
+        // product is not used.
+        batches(IntC<0>{}, IntC<8>{}, t);
         if (sees(t - 1)) {
             const int key = it.key0 + (t - 1) * BN;
-            const char *buf = lds + KBUFS * KBYTES + ((t - 1) % VBUFS) * VBYTES + vread;
-            // values of keys 16 s + 4h .. and 16 s + 8 + 4h .., columns 32 d + r
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const char *at = buf + 16 * s * VROW + 64 * d;
-                    const u2v a = lds_read_tr(at), b = lds_read_tr(at + 8 * VROW);
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(u4v{a.x, a.y, b.x, b.y}), pb[s], o[d], 0, 0, 0);
-                }
-            if (!(there[0] == ~0ull && key >= it.all_lo && key + BN <= it.all_hi)) {
+            if (__builtin_expect(!(there[0] == ~0ull && key >= it.all_lo && key + BN <= it.all_hi), 0)) {
                 unsigned some = 0;
 #pragma unroll
                 for (int w = 0; w < NW; ++w)
-                    some |= nans[(t - 1) % VBUFS][w];
+                    some |= nans[(unsigned)(t - 1) % VBUFS][w];
                 if (uniform(some))
-                    attn_poison<F, D, DT * 4>(p, table, it, key, BN, row, [&](int j, auto &&put) {
-                        v16f &s = o[j >> 2];
-                        const int i = 4 * (j & 3);
-                        float a = s[i], b = s[i + 1], c = s[i + 2], e = s[i + 3];
-                        put(32 * (j >> 2) + 8 * (j & 3) + 4 * h, a, b, c, e);
-                        s[i] = a;
-                        s[i + 1] = b;
-                        s[i + 2] = c;
-                        s[i + 3] = e;
-                    });
+                    poison |= attn_poison<F, D, DT * 4>(p, table, it, key, BN, row,
+                                                        [&](int j) { return 32 * (j >> 2) + 8 * (j & 3) + 4 * h; });
             }
-        }
-        if (sees(t)) {
-            const char *buf = lds + (KBUFS == 1 ? 0 : t % KBUFS) * KBYTES + lane * 16;
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int kt = 0; kt < 2; ++kt) {
-                    const bf16x8v f = as_bf16x8(*reinterpret_cast<const u4v *>(buf + (kt * KS + s) * FS));
-                    if (s == 0)
-                        x[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[s], v16f{}, 0, 0, 0);
-                    else
-                        x[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[s], x[kt], 0, 0, 0);
-                }
         }
     };
     auto softmax = [&](int t) {
         const int key = it.key0 + t * BN;
         if (!(there[0] == ~0ull && key >= lo_most && key + BN <= hi_least)) {
+            const unsigned long long see = (bit_range(row.lo - key, row.hi - key) & there[0]) >> (4 * h);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-                const int kk = 32 * (e >> 4) + 8 * ((e & 15) >> 2) + 4 * h + (e & 3), k = key + kk;
-                const bool see = k >= row.lo && k < row.hi && (there[0] >> kk & 1);
-                x[e >> 4][e & 15] = see ? x[e >> 4][e & 15] : -__builtin_inff();
+                const unsigned half = e < 16 ? (unsigned)see : (unsigned)(see >> 32);
+                x[e >> 4][e & 15] = half >> (8 * ((e & 15) >> 2) + (e & 3)) & 1 ? x[e >> 4][e & 15] : -__builtin_inff();
             }
         }
         float top = -__builtin_inff();
@@ -1028,8 +1143,7 @@ void mx_attn_tile(AttnArgs p)
                 there[a + 1] = loaded;
             }
         }
-        if (AHEAD < T)
-            load(AHEAD);
+        load(AHEAD);
         block_barrier();
         if (NW == 8 && wave >= 4)
             block_barrier();
@@ -1039,14 +1153,21 @@ void mx_attn_tile(AttnArgs p)
 #pragma unroll
             for (int a = 0; a < AHEAD; ++a)
                 there[a] = there[a + 1];
-            if (sees(t))
+            if (sees(t)) {
                 softmax(t);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
+            }
             if (t + AHEAD < T) {
                 expand(t + AHEAD);
                 there[AHEAD] = loaded;
-                if (t + AHEAD + 1 < T)
-                    load(t + AHEAD + 1);
             }
+            // (past the last tile: row 0 of the cache, not used.  Under a
+            // condition the loop would wait for the loads it has just issued,
+            // to merge them with the registers' old contents)
+            load(t + AHEAD + 1);
             block_barrier();
         }
         phase_m(T);
@@ -1054,6 +1175,10 @@ void mx_attn_tile(AttnArgs p)
             block_barrier();
     }
     __syncthreads();
+    if (__builtin_expect(__any(poison != 0), 0))
+#pragma unroll
+        for (int e = 0; e < 16 * DT; ++e)
+            o[e >> 4][e & 15] = poison >> e & 1 ? __builtin_nanf("") : o[e >> 4][e & 15];
 
     l += __shfl_xor(l, 32);
     if (h == 0) {

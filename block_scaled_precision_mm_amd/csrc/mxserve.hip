@@ -183,15 +183,15 @@ AttnFn attn_fn(int which)
     switch (which) {
     case ROWS_16: return &mx_attn_rows<F, D, 1, PAGED>;
     case ROWS_32: return &mx_attn_rows<F, D, 2, PAGED>;
-    case ROWS_128: return &mx_attn_tile<F, D, 4>;
-    default: return &mx_attn_tile<F, D, 8>;
+    case ROWS_128: return &mx_attn_tile<F, D, 4, PAGED>;
+    default: return &mx_attn_tile<F, D, 8, PAGED>;
     }
 }
 
 template <int F, int D>
 AttnFn attn_fn(int which, int64_t page_size)
 {
-    // a load instruction of mx_attn_rows covers 64 chunks of 16 bytes
+    // a wave's load instruction covers 64 chunks of 16 bytes
     return page_size >= 64 / AttnGeom<F, D>::CH ? attn_fn<F, D, 1>(which) : attn_fn<F, D, 0>(which);
 }
 
