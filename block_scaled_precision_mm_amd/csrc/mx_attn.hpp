@@ -29,9 +29,11 @@
 // in any order, and V^T is read in the order in which S^T left them (two
 // transposing LDS reads of four keys each).
 //
-// Rescaling.  m is raised only when a row's maximum passes it by more than
-// 2^8 (a wave-uniform branch): until then p <= 256 relative to m, which FP32
-// sums and BF16's relative precision do not notice.
+// Rescaling.  The p of a tile are taken under the reference so far, and m is
+// raised to the row's maximum only where their sum passes 4096 (a wave-uniform
+// branch that also catches the first tile, where m = -inf makes them infinite
+// or NaN): until then FP32 sums and BF16's relative precision do not notice,
+// and the maximum of a tile need not be found (24 of 115 VALU instructions).
 //
 // Work (plan_item).  Sequence lengths are known on the device only.  A launch
 // has as many workgroups as can run at once plus one per (sequence, head,
@@ -419,7 +421,8 @@ __device__ __forceinline__ float max_across_16(float v)
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-constexpr float kRescale = 8.0f;
+// The largest sum of a lane's p of one tile that keeps the row's reference.
+constexpr float kMostSum = 4096.0f;
 
 // Eight consecutive outputs of a row, d .. d + 7.
 __device__ __forceinline__ void attn_store8(const AttnArgs &p, size_t row, int dim, int d, const float (&f)[8])
@@ -620,7 +623,8 @@ void mx_attn_rows(AttnArgs p)
     unsigned long long poison[QT] = {};
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-        m[t] = -__builtin_inff();
+        // (0 for rows that are not there, whose scores are 0)
+        m[t] = row[t].token >= 0 ? -__builtin_inff() : 0.0f;
         l[t] = 0.0f;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
@@ -713,13 +717,23 @@ void mx_attn_rows(AttnArgs p)
                 for (int e = 0; e < 8; ++e)
                     x[t][e >> 2][e & 3] = see >> (4 * g) >> (16 * (e >> 2) + (e & 3)) & 1 ? x[t][e >> 2][e & 3] : -__builtin_inff();
             }
-            float top = -__builtin_inff();
+            auto weights = [&](float ref) {
+                float sum = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                top = fmaxf(top, x[t][e >> 2][e & 3]);
-            top = max_across_32(max_across_16(top)) * p.c;
-            if (__any(top > m[t] + kRescale)) {
-                const float mn = fmaxf(m[t], top);
+                for (int e = 0; e < 8; ++e) {
+                    const float w = __builtin_amdgcn_exp2f(fmaf(x[t][e >> 2][e & 3], p.c, -ref));
+                    sum += w;
+                    pb[t][e] = (__bf16)w;
+                }
+                return sum;
+            };
+            float sum = weights(m[t]);
+            if (__builtin_expect(__any(!(sum <= kMostSum)), 0)) {
+                float top = -__builtin_inff();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    top = fmaxf(top, x[t][e >> 2][e & 3]);
+                const float mn = fmaxf(m[t], max_across_32(max_across_16(top)) * p.c);
                 const float w = m[t] == mn ? 1.0f : __builtin_amdgcn_exp2f(m[t] - mn);
                 l[t] *= w;
 #pragma unroll
@@ -728,15 +742,10 @@ void mx_attn_rows(AttnArgs p)
                     for (int i = 0; i < 4; ++i)
                         o[t][d][i] *= w;
                 m[t] = mn;
+                // (no key seen yet: m = -inf, every x = -inf, p = 0)
+                sum = weights(mn == -__builtin_inff() ? 0.0f : mn);
             }
-            // (no key seen yet: m = -inf, every x = -inf, p = 0)
-            const float ref = m[t] == -__builtin_inff() ? 0.0f : m[t];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float w = __builtin_amdgcn_exp2f(fmaf(x[t][e >> 2][e & 3], p.c, -ref));
-                l[t] += w;
-                pb[t][e] = (__bf16)w;
-            }
+            l[t] += sum;
         }
         wave_fence();
         // values of keys 4g .. and 16 + 4g .., columns 16 d + r
@@ -842,18 +851,20 @@ __device__ __forceinline__ int value_swizzle(int key)
 }
 
 // Row tiles of 32 NW rows, 32 per wave, over tiles of 64 keys that the waves
-// expand together.  A wave alternates between two phases with a barrier after
-// each:
+// expand together.  A wave alternates between two phases:
 //     M(t)   the second product of tile t - 1 and the first of tile t: MFMA,
 //            fed from LDS
 //     V(t)   the softmax of tile t, expanding a later tile's codes into
 //            LDS, and the loads of one after that: VALU
-// Bound: MFMA, and next to it the softmax's VALU work.  With NW = 8 the two
-// waves of a SIMD are of different groups (waves 0-3 and 4-7), the second
-// half a step behind the first, so one's M runs beside the other's V; tiles
-// are expanded two ahead (by both groups, one phase apart), which takes three
-// buffers of keys and four of values.  With NW = 4 (fewer rows to waste, two
-// workgroups per CU) one tile ahead, one buffer of keys and two of values.
+// Bound: VALU issue (the softmax and the expansion) beside the MFMA.  With
+// NW = 8 the two waves of a SIMD are of different groups (waves 0-3 and 4-7):
+// the one barrier per tile stands behind V for the first and behind M for
+// the second, so one's M runs beside the other's V.  Between barriers k - 1
+// and k the first group is at M(k), V(k), the second at V(k - 1), M(k): they
+// read keys k and values k - 1, and write their parts of tiles k + 2 and
+// k + 1, so four buffers of each (three of keys would do) keep them apart.
+// With NW = 4 (fewer rows to waste, two workgroups per CU): a barrier behind
+// each phase, one tile ahead, one buffer of keys and two of values.
 //
 // v_mfma_f32_32x32x16_bf16, lane (r = l & 31, h = l >> 5): operands row r,
 // k = 8h .. 8h + 7; accumulator column r, register i row 8 (i >> 2) + 4h +
@@ -869,6 +880,25 @@ __device__ __forceinline__ int value_swizzle(int key)
 // busy cycles per tile on conflicts.
 //
 // PAGED as in mx_attn_rows.
+// Tiles of 64 keys from a key on: [first, first + n).
+struct TileRange {
+    int first, n;
+    __device__ __forceinline__ bool has(int t) const { return (unsigned)(t - first) < (unsigned)n; }
+};
+
+// those within keys [lo, hi), and those that hold one of them
+__device__ __forceinline__ TileRange tiles_within(int key0, int lo, int hi)
+{
+    const int a = (max(lo - key0, 0) + 63) / 64, b = hi > key0 ? (hi - key0) / 64 : 0;
+    return {a, max(b - a, 0)};
+}
+
+__device__ __forceinline__ TileRange tiles_touching(int key0, int lo, int hi)
+{
+    const int a = max(lo - key0, 0) / 64, b = hi > key0 ? (hi - key0 + 63) / 64 : 0;
+    return {a, lo < hi ? max(b - a, 0) : 0};
+}
+
 template <int F, int D, int NW, int PAGED>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void mx_attn_tile(AttnArgs p)
@@ -876,7 +906,7 @@ void mx_attn_tile(AttnArgs p)
     constexpr int BM = 32 * NW, BN = 64, THR = 64 * NW;
     using G = AttnGeom<F, D>;
     constexpr int KS = D / 16, DT = D / 32, NP = G::NP;
-    constexpr int AHEAD = NW == 8 ? 2 : 1, KBUFS = NW == 8 ? 3 : 1, VBUFS = NW == 8 ? 4 : 2;
+    constexpr int AHEAD = NW == 8 ? 2 : 1, KBUFS = NW == 8 ? 4 : 1, VBUFS = NW == 8 ? 4 : 2;
     constexpr int FS = 1024 + 4096 / D, KBYTES = 2 * KS * FS, VROW = 2 * D, VBYTES = BN * VROW;
     constexpr int OROW = D + 4;
     constexpr int TILES = KBUFS * KBYTES + VBUFS * VBYTES;
@@ -910,7 +940,8 @@ void mx_attn_tile(AttnArgs p)
         for (int s = 0; s < KS; ++s)
             q[s] = as_bf16x8(row.token >= 0 ? *reinterpret_cast<const u4v *>(src + 16 * s) : u4v{0u, 0u, 0u, 0u});
     }
-    // keys that every row of the wave sees, and keys that some row may see
+    // tiles whose keys every row of the wave sees (of those that are there),
+    // and tiles of which some row may see some
     int lo_most = row.token >= 0 ? row.lo : 0, hi_least = row.token >= 0 ? row.hi : 0x7FFFFFFF;
     int lo_least = row.token >= 0 ? row.lo : 0x7FFFFFFF, hi_most = row.hi;
 #pragma unroll
@@ -920,10 +951,10 @@ void mx_attn_tile(AttnArgs p)
         lo_least = min(lo_least, __shfl_xor(lo_least, d));
         hi_most = max(hi_most, __shfl_xor(hi_most, d));
     }
-    lo_most = uniform(lo_most);
-    hi_least = uniform(hi_least);
-    lo_least = uniform(lo_least);
-    hi_most = uniform(hi_most);
+    const TileRange full = tiles_within(it.key0, uniform(lo_most), uniform(hi_least));
+    const TileRange some = tiles_touching(it.key0, uniform(lo_least), uniform(min(hi_most, it.key1)));
+    const TileRange all_full = tiles_within(it.key0, it.all_lo, it.all_hi);     // of the whole row tile
+    int gone = -1;                          // the last tile expanded so far with keys that are not there
 
     v16f o[DT], x[2];
 #pragma unroll
@@ -931,7 +962,8 @@ void mx_attn_tile(AttnArgs p)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             o[d][i] = 0.0f;
-    float m = -__builtin_inff(), l = 0.0f;
+    // (0 for rows that are not there, whose scores are 0)
+    float m = row.token >= 0 ? -__builtin_inff() : 0.0f, l = 0.0f;
     unsigned long long poison = 0;
     bf16x8v pb[4];
 #pragma unroll
@@ -942,8 +974,6 @@ void mx_attn_tile(AttnArgs p)
     u4v codes[NI];
     unsigned scale[NI];
     unsigned long long loaded = 0;
-    // the keys of the tiles AHEAD .. 0 in front of the softmax that are there
-    unsigned long long there[AHEAD + 1];
     // (threads without a chunk load an earlier one's and do not expand it)
     const bool loads = EVERY || tid < 2 * SIDE;
     const int myside = STATIC ? 0 : uniform(wave * 64 / SIDE);
@@ -987,10 +1017,10 @@ void mx_attn_tile(AttnArgs p)
     };
     // the loaded tile t into its buffers
     auto expand = [&](int t) {
-        const int key = it.key0 + t * BN;
         char *kbuf = lds + (KBUFS == 1 ? 0 : (unsigned)t % KBUFS) * KBYTES;
         char *vbuf = lds + KBUFS * KBYTES + (unsigned)t % VBUFS * VBYTES;
-        const bool whole = loaded == ~0ull && key >= it.all_lo && key + BN <= it.all_hi;
+        gone = loaded == ~0ull ? gone : t;
+        const bool whole = gone != t && all_full.has(t);
         bool nan = false;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -1015,10 +1045,6 @@ void mx_attn_tile(AttnArgs p)
             if (lane == 0)
                 nans[(unsigned)t % VBUFS][wave] = some;
         }
-    };
-    auto sees = [&](int t) {
-        const int key = it.key0 + t * BN;
-        return t >= 0 && t < T && key < hi_most && key + BN > lo_least;
     };
     // this lane's piece of a transposing read: key 4h + (r & 15) / 4 of eight,
     // 8 bytes r & 3 of the 32 at column group r >> 4 (eight keys on, and 64
@@ -1085,36 +1111,47 @@ void mx_attn_tile(AttnArgs p)
         // 0's values for those before it.  Past the last tile the first
         // product is not used.
         batches(IntC<0>{}, IntC<8>{}, t);
-        if (sees(t - 1)) {
-            const int key = it.key0 + (t - 1) * BN;
-            if (__builtin_expect(!(there[0] == ~0ull && key >= it.all_lo && key + BN <= it.all_hi), 0)) {
-                unsigned some = 0;
+        if (__builtin_expect(!(t - 1 > gone && all_full.has(t - 1)) && some.has(t - 1), 0)) {
+            unsigned any = 0;
 #pragma unroll
-                for (int w = 0; w < NW; ++w)
-                    some |= nans[(unsigned)(t - 1) % VBUFS][w];
-                if (uniform(some))
-                    poison |= attn_poison<F, D, DT * 4>(p, table, it, key, BN, row,
-                                                        [&](int j) { return 32 * (j >> 2) + 8 * (j & 3) + 4 * h; });
-            }
+            for (int w = 0; w < NW; ++w)
+                any |= nans[(unsigned)(t - 1) % VBUFS][w];
+            // (of a whole tile in front of one with keys missing: nothing yet)
+            if (uniform(any))
+                poison |= attn_poison<F, D, DT * 4>(p, table, it, it.key0 + (t - 1) * BN, BN, row,
+                                                    [&](int j) { return 32 * (j >> 2) + 8 * (j & 3) + 4 * h; });
         }
     };
     auto softmax = [&](int t) {
-        const int key = it.key0 + t * BN;
-        if (!(there[0] == ~0ull && key >= lo_most && key + BN <= hi_least)) {
-            const unsigned long long see = (bit_range(row.lo - key, row.hi - key) & there[0]) >> (4 * h);
+        if (__builtin_expect(!(t > gone && full.has(t)), 0)) {
+            const int key = it.key0 + t * BN;
+            const unsigned long long there = __ballot(attn_page(p, table, key + lane, it.key1) >= 0);
+            const unsigned long long see = (bit_range(row.lo - key, row.hi - key) & there) >> (4 * h);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
                 const unsigned half = e < 16 ? (unsigned)see : (unsigned)(see >> 32);
                 x[e >> 4][e & 15] = half >> (8 * ((e & 15) >> 2) + (e & 3)) & 1 ? x[e >> 4][e & 15] : -__builtin_inff();
             }
         }
-        float top = -__builtin_inff();
+        // p under the reference so far; where their sum says that it is far
+        // too low (or there is none yet: an infinity or NaN), a new one
+        auto weights = [&](float ref) {
+            float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-            top = fmaxf(top, x[e >> 4][e & 15]);
-        top = max_across_32(top) * p.c;
-        if (__any(top > m + kRescale)) {
-            const float mn = fmaxf(m, top);
+            for (int e = 0; e < 32; ++e) {
+                const float w = __builtin_amdgcn_exp2f(fmaf(x[e >> 4][e & 15], p.c, -ref));
+                sum += w;
+                pb[e >> 3][e & 7] = (__bf16)w;
+            }
+            return sum;
+        };
+        float sum = weights(m);
+        if (__builtin_expect(__any(!(sum <= kMostSum)), 0)) {
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                top = fmaxf(top, x[e >> 4][e & 15]);
+            const float mn = fmaxf(m, max_across_32(top) * p.c);
             const float w = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
             l *= w;
 #pragma unroll
@@ -1123,56 +1160,56 @@ void mx_attn_tile(AttnArgs p)
                 for (int i = 0; i < 16; ++i)
                     o[d][i] *= w;
             m = mn;
+            // (no key seen yet: m = -inf, every x = -inf, p = 0)
+            sum = weights(m == -__builtin_inff() ? 0.0f : m);
         }
-        const float ref = m == -__builtin_inff() ? 0.0f : m;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-            const float w = __builtin_amdgcn_exp2f(fmaf(x[e >> 4][e & 15], p.c, -ref));
-            l += w;
-            pb[e >> 3][e & 7] = (__bf16)w;
-        }
+        l += sum;
     };
 
+    auto phase_v = [&](int t) {
+        if (some.has(t)) {
+            softmax(t);
+        } else {
+            // (p of a tile that no row of the wave sees; and said for x as well,
+            // so that nothing keeps its registers through the other phase)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
+        }
+        if (t + AHEAD < T)
+            expand(t + AHEAD);
+        // (past the last tile: page 0 of the cache, not used.  Under a
+        // condition the loop would wait for the loads it has just issued, to
+        // merge them with the registers' old contents)
+        load(t + AHEAD + 1);
+    };
+    if (lane < VBUFS)
+        nans[lane][wave] = 0;
     if (T > 0) {
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            there[a + 1] = 0;
+        for (int a = 0; a < AHEAD; ++a)
             if (a < T) {
                 load(a);
                 expand(a);
-                there[a + 1] = loaded;
             }
-        }
         load(AHEAD);
         block_barrier();
-        if (NW == 8 && wave >= 4)
-            block_barrier();
-        for (int t = 0; t < T; ++t) {
-            phase_m(t);
-            block_barrier();
-#pragma unroll
-            for (int a = 0; a < AHEAD; ++a)
-                there[a] = there[a + 1];
-            if (sees(t)) {
-                softmax(t);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
+        if (NW == 8 && wave >= 4) {
+            for (int t = 0; t < T; ++t) {
+                phase_m(t);
+                block_barrier();
+                phase_v(t);
             }
-            if (t + AHEAD < T) {
-                expand(t + AHEAD);
-                there[AHEAD] = loaded;
+        } else {
+            for (int t = 0; t < T; ++t) {
+                phase_m(t);
+                if (NW != 8)
+                    block_barrier();
+                phase_v(t);
+                block_barrier();
             }
-            // (past the last tile: row 0 of the cache, not used.  Under a
-            // condition the loop would wait for the loads it has just issued,
-            // to merge them with the registers' old contents)
-            load(t + AHEAD + 1);
-            block_barrier();
         }
         phase_m(T);
-        if (NW == 8 && wave < 4)
-            block_barrier();
     }
     __syncthreads();
     if (__builtin_expect(__any(poison != 0), 0))
