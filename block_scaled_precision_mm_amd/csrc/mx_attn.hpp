@@ -853,18 +853,17 @@ __device__ __forceinline__ int value_swizzle(int key)
 // Row tiles of 32 NW rows, 32 per wave, over tiles of 64 keys that the waves
 // expand together.  A wave alternates between two phases:
 //     M(t)   the second product of tile t - 1 and the first of tile t: MFMA,
-//            fed from LDS
-//     V(t)   the softmax of tile t, expanding a later tile's codes into
-//            LDS, and the loads of one after that: VALU
-// Bound: VALU issue (the softmax and the expansion) beside the MFMA.  With
-// NW = 8 the two waves of a SIMD are of different groups (waves 0-3 and 4-7):
-// the one barrier per tile stands behind V for the first and behind M for
-// the second, so one's M runs beside the other's V.  Between barriers k - 1
-// and k the first group is at M(k), V(k), the second at V(k - 1), M(k): they
-// read keys k and values k - 1, and write their parts of tiles k + 2 and
-// k + 1, so four buffers of each (three of keys would do) keep them apart.
-// With NW = 4 (fewer rows to waste, two workgroups per CU): a barrier behind
-// each phase, one tile ahead, one buffer of keys and two of values.
+//            fed from LDS, and between them expanding tile t + 1's codes
+//            into LDS and the loads of tile t + 2's
+//     V(t)   the softmax of tile t: VALU
+// Bound: MFMA, and beside it VALU issue.  With NW = 8 the two waves of a SIMD
+// are of different groups (waves 0-3 and 4-7): the one barrier per tile
+// stands behind V for the first and behind M for the second, so one's M runs
+// beside the other's V.  Between barriers t - 1 and t both groups are at
+// M(t): they read keys t and values t - 1 and write tile t + 1, so two buffers
+// of keys and three of values keep them apart.  With NW = 4 (fewer rows to
+// waste, two workgroups per CU): a barrier behind each phase, the expansion
+// and the loads in V, one buffer of keys and two of values.
 //
 // v_mfma_f32_32x32x16_bf16, lane (r = l & 31, h = l >> 5): operands row r,
 // k = 8h .. 8h + 7; accumulator column r, register i row 8 (i >> 2) + 4h +
@@ -906,7 +905,7 @@ void mx_attn_tile(AttnArgs p)
     constexpr int BM = 32 * NW, BN = 64, THR = 64 * NW;
     using G = AttnGeom<F, D>;
     constexpr int KS = D / 16, DT = D / 32, NP = G::NP;
-    constexpr int AHEAD = NW == 8 ? 2 : 1, KBUFS = NW == 8 ? 4 : 1, VBUFS = NW == 8 ? 4 : 2;
+    constexpr int KBUFS = NW == 8 ? 2 : 1, VBUFS = NW == 8 ? 3 : 2;
     constexpr int FS = 1024 + 4096 / D, KBYTES = 2 * KS * FS, VROW = 2 * D, VBYTES = BN * VROW;
     constexpr int OROW = D + 4;
     constexpr int TILES = KBUFS * KBYTES + VBUFS * VBYTES;
@@ -983,28 +982,41 @@ void mx_attn_tile(AttnArgs p)
     // rows of the cache per page, and of the pages before this head's
     const int page_rows = p.heads << p.page_shift, head_row = it.head << p.page_shift, in_page = (1 << p.page_shift) - 1;
     const unsigned voff = mykey * G::RB + 16 * chunk, soff = mykey * G::SB + chunk * G::VC / 32;
-    auto load = [&](int t) {
-        const int key = it.key0 + t * BN;
-        const int page = attn_page_of(p, entry, key + lane, it.key1);
+    // loading tile t: which keys are there, chunk i, the next tile's entries
+    int page = -1;
+    auto load_pages = [&](int t) {
+        page = attn_page_of(p, entry, it.key0 + t * BN + lane, it.key1);
         loaded = __ballot(page >= 0);
+    };
+    // (for a page of the cache the row of the wave's first key is a scalar; a
+    // key that is not there: of page 0, in bounds and not used)
+    long long rows_at[NI];
+    auto load_row = [&](int t, int i) {
+        const int key = it.key0 + t * BN, k0 = key_of(i);
+        if constexpr (PAGED)
+            rows_at[i] = (long long)((unsigned long long)(unsigned)max(lane_value(page, k0), 0) * (unsigned)page_rows +
+                                     (unsigned)(head_row + ((key + k0) & in_page)));
+        else
+            rows_at[i] = attn_row_at(p, __shfl(page, k0 + mykey), it.head, key + k0 + mykey);
+    };
+    auto load_codes = [&](int i) {
+        const uint8_t *cp = side_of(i) ? p.codes[1] : p.codes[0];
+        codes[i] = *reinterpret_cast<const u4v *>(cp + rows_at[i] * G::RB + (PAGED ? voff : 16u * chunk));
+    };
+    auto load_scale = [&](int i) {
+        const uint8_t *sp = side_of(i) ? p.scales[1] : p.scales[0];
+        scale[i] = (sp + rows_at[i] * G::SB)[PAGED ? soff : (unsigned)chunk * G::VC / 32];
+    };
+    auto load_entry = [&](int t) { entry = attn_entry(p, table, it.key0 + (t + 1) * BN + lane, it.key1); };
+    auto load = [&](int t) {
+        load_pages(t);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const uint8_t *cp = side_of(i) ? p.codes[1] : p.codes[0], *sp = side_of(i) ? p.scales[1] : p.scales[0];
-            const int k0 = key_of(i);
-            if constexpr (PAGED) {
-                // the row of the wave's first key is a scalar (a key that is
-                // not there: of page 0, in bounds and not used)
-                const unsigned long long at = (unsigned long long)(unsigned)max(lane_value(page, k0), 0) * (unsigned)page_rows +
-                                              (unsigned)(head_row + ((key + k0) & in_page));
-                codes[i] = *reinterpret_cast<const u4v *>(cp + at * G::RB + voff);
-                scale[i] = (sp + at * G::SB)[soff];
-            } else {
-                const long long at = attn_row_at(p, __shfl(page, k0 + mykey), it.head, key + k0 + mykey);
-                codes[i] = *reinterpret_cast<const u4v *>(cp + at * G::RB + 16 * chunk);
-                scale[i] = sp[at * G::SB + chunk * G::VC / 32];
-            }
+            load_row(t, i);
+            load_codes(i);
+            load_scale(i);
         }
-        entry = attn_entry(p, table, key + BN + lane, it.key1);
+        load_entry(t);
     };
     // where this thread's chunks go in a buffer of keys and one of values
     auto put_key = [&](int i, int e) {
@@ -1015,36 +1027,42 @@ void mx_attn_tile(AttnArgs p)
         const int kk = key_of(i) + mykey;
         return kk * VROW + 16 * ((chunk * NP + e) ^ value_swizzle<D>(kk));
     };
-    // the loaded tile t into its buffers
-    auto expand = [&](int t) {
-        char *kbuf = lds + (KBUFS == 1 ? 0 : (unsigned)t % KBUFS) * KBYTES;
-        char *vbuf = lds + KBUFS * KBYTES + (unsigned)t % VBUFS * VBYTES;
-        gone = loaded == ~0ull ? gone : t;
-        const bool whole = gone != t && all_full.has(t);
-        bool nan = false;
+    // piece u of the loaded tile t into its buffer
+    auto expand_piece = [&](int t, int u) {
+        const int i = u / NP, e = u % NP;
+        char *buf = side_of(i) ? lds + KBUFS * KBYTES + (unsigned)t % VBUFS * VBYTES
+                               : lds + (KBUFS == 1 ? 0 : (unsigned)t % KBUFS) * KBYTES;
+        const u2v c = F == FMT_FP4 ? u2v{codes[i][e], 0u} : u2v{codes[i][2 * e & 3], codes[i][(2 * e + 1) & 3]};
+        if (loads)
+            *reinterpret_cast<u4v *>(buf + (side_of(i) ? put_value(i, e) : put_key(i, e))) = mx_decode8<F>(c, scale[i]);
+    };
+    // once its pieces are there: what of its values has to be replaced
+    auto expand_rest = [&](int t) {
+        gone = loaded == ~0ull || t >= T ? gone : t;
+        if (__builtin_expect(!(gone != t && all_full.has(t)), 0)) {
+            char *vbuf = lds + KBUFS * KBYTES + (unsigned)t % VBUFS * VBYTES;
+            bool nan = false;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            u4v w[NP];
-            attn_expand<F>(codes[i], scale[i], w);
-            if (side_of(i) == 0) {
-                if (loads)
-#pragma unroll
-                    for (int e = 0; e < NP; ++e)
-                        *reinterpret_cast<u4v *>(kbuf + put_key(i, e)) = w[e];
-            } else {
-                if (__builtin_expect(!whole, 0))
+            for (int i = 0; i < NI; ++i)
+                if (side_of(i)) {
+                    u4v w[NP];
+                    attn_expand<F>(codes[i], scale[i], w);
                     nan |= attn_clean(w, loaded >> (key_of(i) + mykey) & 1) && loads;
-                if (loads)
+                    if (loads)
 #pragma unroll
-                    for (int e = 0; e < NP; ++e)
-                        *reinterpret_cast<u4v *>(vbuf + put_value(i, e)) = w[e];
-            }
-        }
-        if (__builtin_expect(!whole, 0)) {
+                        for (int e = 0; e < NP; ++e)
+                            *reinterpret_cast<u4v *>(vbuf + put_value(i, e)) = w[e];
+                }
             const unsigned some = __any(nan);
             if (lane == 0)
                 nans[(unsigned)t % VBUFS][wave] = some;
         }
+    };
+    auto expand = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < NI * NP; ++u)
+            expand_piece(t, u);
+        expand_rest(t);
     };
     // this lane's piece of a transposing read: key 4h + (r & 15) / 4 of eight,
     // 8 bytes r & 3 of the 32 at column group r >> 4 (eight keys on, and 64
@@ -1074,43 +1092,80 @@ void mx_attn_tile(AttnArgs p)
                 frag[b % 3][i] = *reinterpret_cast<const u4v *>(at + ((i & 1) * KS + (b - 4) * (DT / 2) + (i >> 1)) * FS);
         }
     };
-    auto multiply = [&](auto bc) {
-        constexpr int b = decltype(bc)::value;
+    // With NW = 8 the M phase also expands tile t + 1 and loads tile t + 2, a
+    // piece behind each of its first MFMAs: they issue while the MFMA runs,
+    // where in the V phase they made it the longer one (V 2200 cycles to M's
+    // 1400).
+    auto between = [&](auto nc, int t) {
+        constexpr int n = decltype(nc)::value;
+        if constexpr (NW == 8) {
+            if constexpr (n % 2 == 1 && n / 2 < NI * NP)
+                expand_piece(t + 1, n / 2);
+            if constexpr (n == 8)
+                expand_rest(t + 1);
+            if constexpr (n == 9)
+                load_pages(t + 2);
+            if constexpr (n == 10)
 #pragma unroll
-        for (int i = 0; i < DT; ++i) {
+                for (int i = 0; i < NI; ++i)
+                    load_row(t + 2, i);
+            if constexpr (n == 11)
+                load_codes(0);
+            if constexpr (n == 12)
+                load_scale(0);
+            if constexpr (n == 13 && NI > 1)
+                load_codes(1);
+            if constexpr (n == 14 && NI > 1)
+                load_scale(1);
+            if constexpr (n == 15)
+                load_entry(t + 2);
+        }
+    };
+    static_assert(NW != 8 || (NI <= 2 && NI * NP <= 4), "pieces in front of the loads");
+    auto multiply = [&](auto bc, int t) {
+        constexpr int b = decltype(bc)::value;
+        static_range<0, DT>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
             const bf16x8v f = as_bf16x8(frag[b % 3][i]);
             if constexpr (b < 4) {
                 o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[b], o[i], 0, 0, 0);
             } else {
-                constexpr int s0 = (b - 4) * (DT / 2);
-                if (s0 + (i >> 1) == 0)
+                constexpr int s = (b - 4) * (DT / 2) + (i >> 1);
+                if constexpr (s == 0)
                     x[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[0], v16f{}, 0, 0, 0);
                 else
-                    x[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[s0 + (i >> 1)], x[i & 1], 0, 0, 0);
+                    x[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, q[s], x[i & 1], 0, 0, 0);
             }
-        }
+            if constexpr (NW == 8) {
+                __builtin_amdgcn_sched_barrier(0);
+                between(IntC<b * DT + i>{}, t);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        });
     };
-    auto batches = [&](auto from, auto upto, int t) {
-        constexpr int B0 = decltype(from)::value, B1 = decltype(upto)::value;
-        fetch(IntC<B0>{}, t);
-        fetch(IntC<B0 + 1>{}, t);
-        __builtin_amdgcn_sched_barrier(0);
-        static_range<B0, B1>([&](auto b) {
+    auto batches = [&](int t) {
+        static_range<0, 8>([&](auto b) {
             constexpr int i = decltype(b)::value;
-            if constexpr (i + 2 < B1)
+            if constexpr (i + 2 < 8)
                 fetch(IntC<i + 2>{}, t);
             __builtin_amdgcn_sched_barrier(0);
-            multiply(b);
+            multiply(b, t);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
     auto phase_m = [&](int t) {
+        if constexpr (NW != 8)
+            fetch(IntC<0>{}, t);
+        fetch(IntC<1>{}, t);
+        // (the MFMAs go first where both waves of a SIMD have something to issue)
+        __builtin_amdgcn_s_setprio(1);
         // No branches, so that the sums stay in their registers: where a wave
         // saw nothing of tile t - 1 its p are zeros, and the values finite (a
         // tile that not every row sees whole holds no NaN); t = 0 takes tile
         // 0's values for those before it.  Past the last tile the first
         // product is not used.
-        batches(IntC<0>{}, IntC<8>{}, t);
+        batches(t);
+        __builtin_amdgcn_s_setprio(0);
         if (__builtin_expect(!(t - 1 > gone && all_full.has(t - 1)) && some.has(t - 1), 0)) {
             unsigned any = 0;
 #pragma unroll
@@ -1167,6 +1222,12 @@ void mx_attn_tile(AttnArgs p)
     };
 
     auto phase_v = [&](int t) {
+        // the first reads of M(t + 1), whose values are there since the last
+        // barrier: at its start all four waves would wait for them
+        if constexpr (NW == 8) {
+            fetch(IntC<0>{}, t + 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         if (some.has(t)) {
             softmax(t);
         } else {
@@ -1176,24 +1237,23 @@ void mx_attn_tile(AttnArgs p)
             for (int i = 0; i < 4; ++i)
                 pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
         }
-        if (t + AHEAD < T)
-            expand(t + AHEAD);
-        // (past the last tile: page 0 of the cache, not used.  Under a
-        // condition the loop would wait for the loads it has just issued, to
-        // merge them with the registers' old contents)
-        load(t + AHEAD + 1);
+        // (loads past the last tile are of page 0 of the cache and not used.
+        // Under a condition the loop would wait for the loads it has just
+        // issued, to merge them with the registers' old contents)
+        if constexpr (NW != 8) {
+            expand(t + 1);
+            load(t + 2);
+        }
     };
     if (lane < VBUFS)
         nans[lane][wave] = 0;
     if (T > 0) {
-#pragma unroll
-        for (int a = 0; a < AHEAD; ++a)
-            if (a < T) {
-                load(a);
-                expand(a);
-            }
-        load(AHEAD);
+        load(0);
+        expand(0);
+        load(1);
         block_barrier();
+        if constexpr (NW == 8)
+            fetch(IntC<0>{}, 0);
         if (NW == 8 && wave >= 4) {
             for (int t = 0; t < T; ++t) {
                 phase_m(t);
