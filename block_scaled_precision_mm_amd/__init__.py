@@ -133,9 +133,13 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
+# the current stream's handle without the Stream object around it (3 us a call)
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -177,12 +181,14 @@ def _workspace(ws, nbytes, stream_ptr):
         return ws.data_ptr(), ws.numel() * ws.element_size()
     if ws != "auto":
         raise ValueError("workspace must be a tensor, None or 'auto'")
-    key = (torch.cuda.current_device(), stream_ptr)
-    t = _WORKSPACES.get(key)
-    if t is None or t.numel() < nbytes:
-        t = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
-        _WORKSPACES[key] = t
-    return t.data_ptr(), t.numel()
+    key = (_current_device(), stream_ptr)
+    held = _WORKSPACES.get(key)
+    if held is None or held.numel() < nbytes:
+        # filled and, later, given back to the allocator on the stream that uses it
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream_ptr)):
+            held = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+        _WORKSPACES[key] = held
+    return held.data_ptr(), held.numel()
 
 
 def mx_scaled_mm_workspace_bytes(is_fp4, M, N, K) -> int:
@@ -511,6 +517,17 @@ def mx_noalloc_scratch_bytes() -> int:
 
 
 # ------------------------------------------------- around the products
+_BF16 = torch.bfloat16
+
+
+def _bf16_of(name, t, n):
+    """t: a contiguous bfloat16 CUDA tensor of n elements, a raw pointer or None."""
+    if t is None or t.__class__ is int:
+        return
+    if t.dtype is not _BF16 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError("%s must be a contiguous bfloat16 CUDA tensor of %d elements" % (name, n))
+
+
 def mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, stream=None) -> None:
     """RMSNorm with the residual's addition (C ABI mx_rmsnorm): x, residual
     (or None) and h (or None) bfloat16 [rows][K], weight bfloat16 [K] or None.
@@ -518,27 +535,26 @@ def mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, 
     [rows][K] or E2M1 pairs [rows][K/2] with y_scale uint8 [rows][K/32]; a
     1-byte y takes its format from its size unless out_kind is given."""
     n = rows * K
-    for name, t in (("x", x), ("residual", residual), ("h", h)):
-        if isinstance(t, torch.Tensor):
-            if not t.is_cuda or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.numel() != n:
-                raise ValueError("%s must be a contiguous bfloat16 CUDA tensor of rows*K elements" % name)
-    if isinstance(weight, torch.Tensor):
-        if not weight.is_cuda or weight.dtype != torch.bfloat16 or not weight.is_contiguous() or weight.numel() != K:
-            raise ValueError("weight must be a contiguous bfloat16 CUDA tensor of K elements")
-    if out_kind is None:
-        if not isinstance(y, torch.Tensor):
-            raise ValueError("out_kind is required when y is a raw pointer")
-        out_kind = _OUT_OF_DTYPE.get(y.dtype)
+    _bf16_of("x", x, n)
+    _bf16_of("residual", residual, n)
+    _bf16_of("h", h, n)
+    _bf16_of("weight", weight, K)
+    if y.__class__ is int:
         if out_kind is None:
-            out_kind = OUT_MXFP8 if y.numel() == n else OUT_MXFP4
-    if isinstance(y, torch.Tensor):
-        m, size = {OUT_BF16: (n, 2), OUT_F16: (n, 2), OUT_F32: (n, 4), OUT_MXFP4: (n // 2, 1)}.get(out_kind, (n, 1))
-        if not y.is_cuda or not y.is_contiguous() or y.numel() != m or y.element_size() != size:
-            raise ValueError("y must be a contiguous CUDA tensor of %d elements of %d bytes" % (m, size))
-    if isinstance(y_scale, torch.Tensor):
-        if not y_scale.is_cuda or not y_scale.is_contiguous() or y_scale.element_size() != 1 or \
-                y_scale.numel() != rows * (K // 32):
-            raise ValueError("y_scale must be a contiguous 1-byte CUDA tensor of rows*K/32 elements")
+            raise ValueError("out_kind is required when y is a raw pointer")
+    else:
+        size = y.element_size()
+        if out_kind is None:
+            out_kind = _OUT_OF_DTYPE.get(y.dtype)
+            if out_kind is None:
+                out_kind = OUT_MXFP8 if y.numel() == n else OUT_MXFP4
+        if not y.is_cuda or not y.is_contiguous() or size != (2, 2, 4, 1, 1)[out_kind] or \
+                y.numel() != (n // 2 if out_kind == OUT_MXFP4 else n):
+            raise ValueError("y must be a contiguous CUDA tensor of rows*K values of its output kind")
+    if y_scale is not None and y_scale.__class__ is not int and (
+            not y_scale.is_cuda or not y_scale.is_contiguous() or y_scale.element_size() != 1 or
+            y_scale.numel() != rows * (K // 32)):
+        raise ValueError("y_scale must be a contiguous 1-byte CUDA tensor of rows*K/32 elements")
     st = _lib.mx_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y), _ptr(y_scale), rows, K, eps,
                          out_kind, _stream(stream))
     if st:
@@ -609,15 +625,18 @@ class KVCache:
 def _token_rows(name, t, tokens, heads, dim):
     """Stride between the tokens of a bfloat16 [tokens][heads][dim] tensor
     whose tokens may be apart (a part of the rows of a joint product)."""
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.shape != (tokens, heads, dim) or \
-            (t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim))):
-        raise ValueError("%s must be a bfloat16 CUDA tensor [%d][%d][%d], each token's values contiguous"
-                         % (name, tokens, heads, dim))
-    return t.stride(0) if tokens > 1 else heads * dim
+    if t.dtype is not _BF16 or not t.is_cuda or t.shape != (tokens, heads, dim):
+        raise ValueError("%s must be a bfloat16 CUDA tensor [%d][%d][%d]" % (name, tokens, heads, dim))
+    if tokens == 0:
+        return heads * dim
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
+        raise ValueError("%s must hold each token's values contiguously" % name)
+    return s0 if tokens > 1 else heads * dim
 
 
 def _cache_call(fn, name, cache, k, v, slots, stream):
-    if not slots.is_cuda or slots.dtype != torch.int64 or not slots.is_contiguous() or slots.dim() != 1:
+    if slots.dtype is not torch.int64 or not slots.is_cuda or slots.dim() != 1 or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous one-dimensional int64 CUDA tensor")
     n = slots.shape[0]
     ks = _token_rows("k", k, n, cache.kv_heads, cache.head_dim)
@@ -645,7 +664,7 @@ def mx_paged_attention_workspace_bytes(cache, seqs, tokens, q_heads, max_new) ->
 
 
 def _int32(name, t, shape):
-    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.shape != shape:
+    if t.dtype is not torch.int32 or not t.is_cuda or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 CUDA tensor of shape %s" % (name, tuple(shape)))
 
 
@@ -667,10 +686,11 @@ def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, c
     if table.dim() != 2:
         raise ValueError("table must be [seqs][pages of a sequence]")
     _int32("table", table, (seqs, table.shape[1]))
-    if not out.is_cuda or not out.is_contiguous() or out.shape != q.shape or out.dtype not in _OUT_OF_DTYPE:
+    kind = _OUT_OF_DTYPE.get(out.dtype)
+    if kind is None or not out.is_cuda or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous CUDA tensor of q's shape in BF16, FP16 or FP32")
-    if lse is not None and (not lse.is_cuda or lse.dtype != torch.float32 or not lse.is_contiguous() or
-                            lse.shape != (tokens, heads)):
+    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_cuda or lse.shape != (tokens, heads) or
+                            not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 CUDA tensor [tokens][q_heads]")
     if max_new is None:
         max_new = tokens
@@ -680,7 +700,7 @@ def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, c
     st = _lib.mx_paged_attention(cache._ref, q.data_ptr(), qs, ends.data_ptr(), lens.data_ptr(), table.data_ptr(),
                                  table.shape[1], seqs, tokens, heads, max_new,
                                  dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
-                                 _OUT_OF_DTYPE[out.dtype], 0 if lse is None else lse.data_ptr(), wp, wb, st_ptr)
+                                 kind, 0 if lse is None else lse.data_ptr(), wp, wb, st_ptr)
     if st:
         raise MxGemmError(st, "mx_paged_attention")
 

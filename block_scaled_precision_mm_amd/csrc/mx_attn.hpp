@@ -441,72 +441,92 @@ __device__ __forceinline__ void attn_store8(const AttnArgs &p, size_t row, int d
     }
 }
 
-// Bytes of the workspace slot of a part of a tile of `rows` rows (a multiple
-// of 128 bytes): the threads' runs of eight sums, 512 threads from 256 rows
-// on and 256 below, and (m, l) of each row.
-constexpr int attn_slot_bytes(int rows, int dim)
-{
-    const int threads = rows >= 256 ? 512 : 256;
-    return cdiv_c(rows * dim / 8, threads) * threads * 32 + cdiv_c(rows * 8, 128) * 128;
-}
+// Bytes of the workspace slot of a part of a tile of `rows` rows: the sums
+// [rows][dim], then (m, l) of each row; a multiple of 128.
+constexpr int attn_slot_bytes(int rows, int dim) { return rows * dim * 4 + cdiv_c(rows * 8, 128) * 128; }
 
-// The end of a row tile.  Its NR x D sums lie with the threads of the
-// workgroup as runs of eight columns: run u of thread `tid` is columns
-// 8 (i % (D / 8)) .. + 7 of row i / (D / 8), i = tid + u * NTHR (below the
-// number of runs).  get(u, f, m, l): the run's sums, the row's reference and
-// sum of p.  Writes outputs and lse, or for a split row tile the part,
-// and the whole in the workgroup that arrives last.
-template <int D, int NR, int NTHR, class Get>
-__device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &it, int tid, Get &&get)
-{
-    constexpr int RUNS = D / 8, NU = cdiv_c(NR * RUNS, NTHR);
-    constexpr bool EVEN = NR * RUNS % NTHR == 0;
-    auto mine_is = [&](int u) { return EVEN || tid + u * NTHR < NR * RUNS; };
-    auto write = [&](int u, float (&f)[8], float m, float l) {
-        const int i = tid + u * NTHR, run = i % RUNS;
-        const AttnRow r = attn_row(p, it, it.row0 + i / RUNS);
-        if (r.token < 0)
-            return;
-        const size_t row = (size_t)(it.tok0 + r.token) * (p.heads * p.group) + it.head * p.group + r.head;
-        // (a row that sees no key has l = 0 and sums 0; a NaN is not 0)
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+// Eight sums of a row relative to m, and the sum of its p.
+struct AttnSums {
+    float f[8], m, l;
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            f[e] *= inv;
-        attn_store8(p, row, D, 8 * run, f);
+            f[e] = 0.0f;
+        m = -__builtin_inff();
+        l = 0.0f;
+    }
+    // (sums of keys that the row does not see: m = -inf, l = 0, f = 0)
+    __device__ __forceinline__ void add(const float (&g)[8], float mq, float lq)
+    {
+        const float mn = fmaxf(m, mq);
+        const float wa = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+        const float wb = mq == mn ? 1.0f : __builtin_amdgcn_exp2f(mq - mn);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = f[e] * wa + g[e] * wb;
+        l = l * wa + lq * wb;
+        m = mn;
+    }
+};
+
+// The end of a row tile.  Its sums lie with the threads of the workgroup as
+// runs of eight columns: run u of thread `tid` is columns 8 (i % (D / 8)) ..
+// + 7 of row i / (D / 8), i = tid + u * NTHR, for the rows that are there.
+// get(u, sums): the run's sums.  Writes outputs and lse, or for a split row
+// tile the part, and the whole in the workgroup that arrives last.
+//
+// That workgroup reads parts * rows * D sums alone, one memory latency after
+// the other, which for one sequence's few rows cost more than the keys (4
+// rows of 64 parts 30 of 64 us): so parts hold only the rows that are there,
+// and where these leave threads over, two or four groups of threads take
+// every second or fourth part each and are joined in `scratch` (of 40 NTHR
+// bytes of LDS that nothing else uses any more).
+template <int D, int NR, int NTHR, class Get>
+__device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &it, int tid, float *scratch, Get &&get)
+{
+    constexpr int RUNS = D / 8, NU = cdiv_c(NR * RUNS, NTHR);
+    const int nrows = min(NR, it.ntok * p.group - it.row0), n = nrows * RUNS;
+    auto write = [&](int i, AttnSums &s) {
+        const int run = i % RUNS;
+        const AttnRow r = attn_row(p, it, it.row0 + i / RUNS);
+        const size_t row = (size_t)(it.tok0 + r.token) * (p.heads * p.group) + it.head * p.group + r.head;
+        // (a row that sees no key has l = 0 and sums 0; a NaN is not 0)
+        const float inv = s.l == 0.0f ? 0.0f : 1.0f / s.l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            s.f[e] *= inv;
+        attn_store8(p, row, D, 8 * run, s.f);
         if (p.lse && run == 0)
-            p.lse[row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+            p.lse[row] = s.l == 0.0f ? -__builtin_inff() : (s.m + __builtin_amdgcn_logf(s.l)) * 0.6931471805599453f;
     };
     if (it.parts == 1) {
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            if (!mine_is(u))
-                continue;
-            float f[8], m, l;
-            get(u, f, m, l);
-            write(u, f, m, l);
-        }
+        for (int u = 0; u < NU; ++u)
+            if (tid + u * NTHR < n) {
+                AttnSums s;
+                get(u, s);
+                write(tid + u * NTHR, s);
+            }
         return;
     }
-    // slot: [NU][2][NTHR] four sums, then [NR] (m, l)
-    constexpr int SUMS = NU * NTHR * 32, SLOT = attn_slot_bytes(NR, D), DEV = 16;
-    static_assert(SLOT >= SUMS + NR * 8, "slot");
+    constexpr int SUMS = NR * D * 4, SLOT = attn_slot_bytes(NR, D), DEV = 16;
     __shared__ unsigned arrived;
     const __amdgpu_buffer_rsrc_t mine =
         make_rsrc(p.parts + (size_t)(it.slot + it.part * it.slot_step) * SLOT, (unsigned)SLOT);
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-        if (!mine_is(u))
-            continue;
-        float f[8], m, l;
-        get(u, f, m, l);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v4f{f[0], f[1], f[2], f[3]}), mine,
-                                               (unsigned)(((2 * u) * NTHR + tid) * 16), 0, DEV);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v4f{f[4], f[5], f[6], f[7]}), mine,
-                                               (unsigned)(((2 * u + 1) * NTHR + tid) * 16), 0, DEV);
         const int i = tid + u * NTHR;
+        if (i >= n)
+            continue;
+        AttnSums s;
+        get(u, s);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v4f{s.f[0], s.f[1], s.f[2], s.f[3]}), mine,
+                                               (unsigned)(i * 32), 0, DEV);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v4f{s.f[4], s.f[5], s.f[6], s.f[7]}), mine,
+                                               (unsigned)(i * 32 + 16), 0, DEV);
         if (i % RUNS == 0)
-            __builtin_amdgcn_raw_buffer_store_b64(u2v{__float_as_uint(m), __float_as_uint(l)}, mine,
+            __builtin_amdgcn_raw_buffer_store_b64(u2v{__float_as_uint(s.m), __float_as_uint(s.l)}, mine,
                                                   (unsigned)(SUMS + i / RUNS * 8), 0, DEV);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -516,45 +536,62 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
     __syncthreads();
     if (arrived != (unsigned)(it.parts - 1))
         return;
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-        if (!mine_is(u))
-            continue;
-        const int row = (tid + u * NTHR) / RUNS;
-        float f[8] = {0, 0, 0, 0, 0, 0, 0, 0}, m = -__builtin_inff(), l = 0.0f;
+    // parts first, first + step, .. of run i
+    auto sum_parts = [&](int i, int first, int step, AttnSums &s) {
+        s.clear();
         constexpr int PF = 8;       // parts in flight
-        for (int q0 = 0; q0 < it.parts; q0 += PF) {
+        for (int q0 = first; q0 < it.parts; q0 += PF * step) {
             u4v a[PF], b[PF];
             u2v ml[PF];
 #pragma unroll
             for (int q = 0; q < PF; ++q) {
-                const int part = min(q0 + q, it.parts - 1);
+                const int part = min(q0 + q * step, it.parts - 1);
                 const __amdgpu_buffer_rsrc_t src =
                     make_rsrc(p.parts + (size_t)(it.slot + part * it.slot_step) * SLOT, (unsigned)SLOT);
-                ml[q] = __builtin_amdgcn_raw_buffer_load_b64(src, (unsigned)(SUMS + row * 8), 0, DEV);
-                a[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(((2 * u) * NTHR + tid) * 16), 0, DEV);
-                b[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(((2 * u + 1) * NTHR + tid) * 16), 0, DEV);
+                ml[q] = __builtin_amdgcn_raw_buffer_load_b64(src, (unsigned)(SUMS + i / RUNS * 8), 0, DEV);
+                a[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(i * 32), 0, DEV);
+                b[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(i * 32 + 16), 0, DEV);
             }
 #pragma unroll
-            for (int q = 0; q < PF; ++q) {
-                if (q0 + q >= it.parts)
-                    break;
-                const float mq = __uint_as_float(ml[q][0]), lq = __uint_as_float(ml[q][1]);
-                const float mn = fmaxf(m, mq);
-                // (a part whose keys the row does not see has m = -inf and no sums)
-                const float wa = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-                const float wb = mq == mn ? 1.0f : __builtin_amdgcn_exp2f(mq - mn);
-                const v4f fa = __builtin_bit_cast(v4f, a[q]), fb = __builtin_bit_cast(v4f, b[q]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[e] = f[e] * wa + fa[e] * wb;
-                    f[4 + e] = f[4 + e] * wa + fb[e] * wb;
+            for (int q = 0; q < PF; ++q)
+                if (q0 + q * step < it.parts) {
+                    const v4f fa = __builtin_bit_cast(v4f, a[q]), fb = __builtin_bit_cast(v4f, b[q]);
+                    s.add({fa[0], fa[1], fa[2], fa[3], fb[0], fb[1], fb[2], fb[3]}, __uint_as_float(ml[q][0]),
+                          __uint_as_float(ml[q][1]));
                 }
-                l = l * wa + lq * wb;
-                m = mn;
+        }
+    };
+    const int groups = n <= NTHR / 4 ? 4 : n <= NTHR / 2 ? 2 : 1;
+    if (groups > 1) {
+        // (whole waves per group: `first` is a scalar)
+        const int each = NTHR / groups, group = uniform(tid / each), i = tid - group * each;
+        AttnSums s;
+        if (i < n) {
+            sum_parts(i, group, groups, s);
+            if (group > 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    scratch[e * NTHR + tid] = s.f[e];
+                scratch[8 * NTHR + tid] = s.m;
+                scratch[9 * NTHR + tid] = s.l;
             }
         }
-        write(u, f, m, l);
+        __syncthreads();
+        if (group == 0 && i < n) {
+            for (int o = 1; o < groups; ++o) {
+                const float *src = scratch + o * each + i;
+                s.add({src[0], src[NTHR], src[2 * NTHR], src[3 * NTHR], src[4 * NTHR], src[5 * NTHR], src[6 * NTHR], src[7 * NTHR]},
+                      src[8 * NTHR], src[9 * NTHR]);
+            }
+            write(i, s);
+        }
+    } else {
+#pragma unroll 1
+        for (int i = tid; i < n; i += NTHR) {
+            AttnSums s;
+            sum_parts(i, 0, 1, s);
+            write(i, s);
+        }
     }
     if (tid == 0)
         __hip_atomic_store(p.counters + it.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -563,31 +600,38 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
 // ------------------------------------------------------------ few rows
 // Row tiles of 16 QT rows.  The four waves of a workgroup take turns at tiles
 // of 32 keys, each with its own sums, its own LDS and no barrier in the loop;
-// the sums are joined at the end.  Bound: HBM, the cache's bytes; the next
-// tile's codes are in flight while one is worked on.
+// the sums are joined at the end.  Bound: HBM, the cache's bytes, and close
+// behind it (for MXFP4 codes before it) the VALU work of expanding them; the
+// next tile's codes are in flight while one is worked on.
 //
 // v_mfma_f32_16x16x32_bf16, lane (r = l & 15, g = l >> 4): operands row r,
 // k = 8g .. 8g + 7; accumulator column r, rows 4g .. 4g + 3.  So S^T tile kt
 // (keys 16 kt ..) leaves lane (r, g) with keys 16 kt + 4g + i of query row r,
 // and P^T's eight k of lane group g are keys 4g + i and 16 + 4g + i.
 //
-// LDS of a wave: the keys' tile as operand fragments (lane order, 1 KB each,
-// so the reads are contiguous), then, in the same place, the values' tile
-// as rows of 2D + 32 bytes (the 32 spread the four keys and four lane groups
-// of a transposing read over the banks).
+// Keys go from memory to the MFMA without LDS: lane (r, g) loads the g-th
+// quarter of key r's row (for 128 bytes, 16 bytes of each half), and step s
+// of the product takes eight values of that piece, d = column(s, g) .. + 7;
+// q is loaded in the same order of d.  (16 rows in consecutive lanes cost the
+// address unit three times a contiguous load, which is still twice what HBM
+// delivers; through LDS the keys took 8 writes, 8 reads and a round trip per
+// tile.)
 //
-// PAGED: pages hold at least the KPL keys of one load instruction, so the
-// page is a scalar and the lanes' offsets are the same for every tile.
+// Values are expanded into LDS as rows of 2D + 32 bytes and read transposed
+// (the 32 spread the four keys and four lane groups of a read over the banks).
+//
+// PAGED: pages of 16 keys or more, so that the two pages of a tile are
+// scalars and the lanes' offsets the same for every tile.
 template <int F, int D, int QT, int PAGED>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(QT == 1 ? 3 : 2)))
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(QT > 1 ? 2 : F == FMT_FP8 && D == 128 ? 3 : 4)))
 void mx_attn_rows(AttnArgs p)
 {
     constexpr int KT = 32, BM = 16 * QT, BN = 4 * KT;
     using G = AttnGeom<F, D>;
     constexpr int KS = D / 32, DT = D / 16, NP = G::NP;
-    constexpr int KPL = 64 / G::CH, NL = KT / KPL;      // keys per load, loads per tile
-    constexpr int KBYTES = 2 * KS * 1024, VROW = 2 * D + 32, VBYTES = KT * VROW;
-    constexpr int WBYTES = KBYTES > VBYTES ? KBYTES : VBYTES;
+    constexpr int KPL = 64 / G::CH, NL = KT / KPL;      // values: keys per load, loads per tile
+    constexpr int KQ = G::RB / 4;                       // bytes of a key's row per lane: 8, 16 or 2 x 16
+    constexpr int VROW = 2 * D + 32, WBYTES = KT * VROW;
     constexpr int OROW = D + 4;                         // floats of a row of sums in LDS
     constexpr int OBYTES = 16 * OROW * 4;               // one wave's 16 rows
     constexpr int BYTES = (WBYTES > OBYTES ? WBYTES : OBYTES) * 4;
@@ -600,21 +644,24 @@ void mx_attn_rows(AttnArgs p)
         return;
 
     const int *table = p.table + it.seq * p.table_stride;
-    const int mykey = lane / G::CH, chunk = lane % G::CH;
     int key = it.key0 + wave * KT;
     // table entry of key `lane & 31` of the next tile loaded
     int entry = it.key0 < it.key1 ? attn_entry(p, table, key + (lane & 31), it.key1) : -1;
 
+    // first of the eight columns that step s takes from this lane
+    auto column = [&](int s) {
+        return F == FMT_FP4 ? (D / 4) * g + 8 * s : D == 128 ? (s >> 1) * 64 + 16 * g + 8 * (s & 1) : (D / 4) * g + 8 * s;
+    };
     AttnRow row[QT];
     bf16x8v q[QT][KS];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         row[t] = attn_row(p, it, it.row0 + 16 * t + r);
         const uint16_t *src = p.q + (long long)(it.tok0 + max(row[t].token, 0)) * p.q_stride +
-                              (long long)(it.head * p.group + row[t].head) * D + 8 * g;
+                              (long long)(it.head * p.group + row[t].head) * D;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-            q[t][s] = as_bf16x8(row[t].token >= 0 ? *reinterpret_cast<const u4v *>(src + 32 * s) : u4v{0u, 0u, 0u, 0u});
+            q[t][s] = as_bf16x8(row[t].token >= 0 ? *reinterpret_cast<const u4v *>(src + column(s)) : u4v{0u, 0u, 0u, 0u});
     }
 
     char *mem = lds + wave * WBYTES;
@@ -631,30 +678,60 @@ void mx_attn_rows(AttnArgs p)
             o[t][d] = v4f{0, 0, 0, 0};
     }
 
-    // codes and scale codes of this lane's chunks of the next tile, and the
-    // keys of it that are there (bits)
-    u4v kc[NL], vc[NL];
-    unsigned ks[NL], vs[NL], there = 0;
-    const unsigned voff = mykey * G::RB + chunk * 16, soff = mykey * G::SB + chunk * G::VC / 32;
+    // The next tile: this lane's pieces of keys r and 16 + r with the row's
+    // scale codes, its chunks of values (key mykey + j KPL) with theirs, and
+    // the keys of it that are there (bits).
+    u4v kc[2][2], vc[NL];
+    unsigned ks[2], vs[NL], there = 0;
+    const int mykey = lane / G::CH, chunk = lane % G::CH;
     auto load = [&](int k) {
         const int page = attn_page_of(p, entry, k + (lane & 31), it.key1);
         there = (unsigned)__ballot(page >= 0);
+        // rows of the cache of keys 0 and 16 of the tile
+        long long at0 = 0, at1 = 0;
+        if constexpr (PAGED) {
+            at0 = attn_row_at(p, lane_value(page, 0), it.head, k);
+            at1 = attn_row_at(p, lane_value(page, 16), it.head, k + 16);
+        }
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            long long at = kt ? at1 : at0;
+            unsigned off = r;                           // rows on from there
+            if constexpr (!PAGED) {
+                at = attn_row_at(p, __shfl(page, 16 * kt + r), it.head, k + 16 * kt + r);
+                off = 0;
+            }
+            const uint8_t *c = p.codes[0] + at * G::RB, *s = p.scales[0] + at * G::SB;
+            if constexpr (KQ == 8) {
+                const u2v w = *reinterpret_cast<const u2v *>(c + (off * G::RB + 8 * g));
+                kc[kt][0] = u4v{w.x, w.y, 0u, 0u};
+            } else {
+                kc[kt][0] = *reinterpret_cast<const u4v *>(c + (off * G::RB + 16 * g));
+                if constexpr (KQ == 32)
+                    kc[kt][1] = *reinterpret_cast<const u4v *>(c + (off * G::RB + 64 + 16 * g));
+            }
+            if constexpr (G::SB == 4)
+                ks[kt] = *reinterpret_cast<const unsigned *>(s + off * 4);
+            else
+                ks[kt] = *reinterpret_cast<const uint16_t *>(s + off * 2);
+        }
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
-            if constexpr (PAGED) {
-                // scalar row of the first key of the load
-                const long long at = attn_row_at(p, lane_value(page, j * KPL), it.head, k + j * KPL);
-                kc[j] = *reinterpret_cast<const u4v *>(p.codes[0] + at * G::RB + voff);
-                vc[j] = *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + voff);
-                ks[j] = p.scales[0][at * G::SB + soff];
-                vs[j] = p.scales[1][at * G::SB + soff];
+            const int kk = mykey + j * KPL;
+            long long at;
+            unsigned off;
+            if constexpr (!PAGED) {
+                at = attn_row_at(p, __shfl(page, kk), it.head, k + kk);
+                off = 0;
+            } else if constexpr (KPL <= 16) {
+                at = j * KPL < 16 ? at0 : at1;
+                off = kk & 15;
             } else {
-                const long long at = attn_row_at(p, __shfl(page, mykey + j * KPL), it.head, k + mykey + j * KPL);
-                kc[j] = *reinterpret_cast<const u4v *>(p.codes[0] + at * G::RB + chunk * 16);
-                vc[j] = *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + chunk * 16);
-                ks[j] = p.scales[0][at * G::SB + chunk * G::VC / 32];
-                vs[j] = p.scales[1][at * G::SB + chunk * G::VC / 32];
+                at = kk < 16 ? at0 : at1;
+                off = kk & 15;
             }
+            vc[j] = *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + (off * G::RB + 16 * chunk));
+            vs[j] = (p.scales[1] + at * G::SB)[off * G::SB + chunk * G::VC / 32];
         }
         entry = attn_entry(p, table, k + BN + (lane & 31), it.key1);
     };
@@ -664,33 +741,10 @@ void mx_attn_rows(AttnArgs p)
     };
     if (key < it.key1)
         load(key);
-    // piece (chunk * NP + e) of a key's D / 8 is one lane's operand of one step
-    char *kput = mem + (((chunk * NP) >> 2) * 64 + ((chunk * NP) & 3) * 16) * 16;
     char *vput = mem + mykey * VROW + chunk * G::VC * 2;
     const char *vread = mem + (4 * g + (r >> 2)) * VROW + (r & 3) * 8;
     for (; key < it.key1; key += BN) {
-#pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            u4v w[NP];
-            attn_expand<F>(kc[j], ks[j], w);
-            const int kk = mykey + j * KPL;
-#pragma unroll
-            for (int e = 0; e < NP; ++e)
-                *reinterpret_cast<u4v *>(kput + ((kk >> 4) * KS * 64 + e * 16 + (kk & 15)) * 16) = w[e];
-        }
-        wave_fence();
-        v4f x[QT][2];
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
-                const bf16x8v f = as_bf16x8(*reinterpret_cast<const u4v *>(mem + ((kt * KS + s) * 64 + lane) * 16));
-#pragma unroll
-                for (int t = 0; t < QT; ++t)
-                    x[t][kt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, q[t][s], s ? x[t][kt] : v4f{0, 0, 0, 0}, 0, 0, 0);
-            }
-        wave_fence();
-        // values into the same place, then the next tile's codes on their way
+        // values into LDS
         const bool whole = there == 0xFFFFFFFFu && key >= it.all_lo && key + KT <= it.all_hi;
         const unsigned here = there;
         bool nan = false;
@@ -698,12 +752,30 @@ void mx_attn_rows(AttnArgs p)
         for (int j = 0; j < NL; ++j) {
             u4v w[NP];
             attn_expand<F>(vc[j], vs[j], w);
-            if (!whole)
+            if (__builtin_expect(!whole, 0))
                 nan |= attn_clean(w, here >> (mykey + j * KPL) & 1);
 #pragma unroll
             for (int e = 0; e < NP; ++e)
                 *reinterpret_cast<u4v *>(vput + j * KPL * VROW + 16 * e) = w[e];
         }
+        // scores: step s takes piece s & 1 (of an E4M3 chunk) or s & 3
+        v4f x[QT][2];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                u4v w;
+                if constexpr (F == FMT_FP4) {
+                    const unsigned byte = D == 128 ? ks[kt] >> (8 * g) & 255u : ks[kt] >> (8 * (g >> 1)) & 255u;
+                    w = mx_decode8<F>(u2v{kc[kt][0][s], 0u}, byte);
+                } else {
+                    const unsigned byte = ks[kt] >> (8 * (g >> 1) + (D == 128 ? 16 * (s >> 1) : 0)) & 255u;
+                    w = mx_decode8<F>(u2v{kc[kt][s >> 1][2 * (s & 1)], kc[kt][s >> 1][2 * (s & 1) + 1]}, byte);
+                }
+#pragma unroll
+                for (int t = 0; t < QT; ++t)
+                    x[t][kt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(w), q[t][s], s ? x[t][kt] : v4f{0, 0, 0, 0}, 0, 0, 0);
+            }
         // (past the last key: row 0 of the cache, not used.  Under a condition
         // the loop would wait for the loads it has just issued, to merge them
         // with the registers' old contents)
@@ -831,12 +903,13 @@ void mx_attn_rows(AttnArgs p)
         }
         __syncthreads();
     }
-    attn_finish<D, BM, 256>(p, it, tid, [&](int u, float (&out)[8], float &mm, float &ll) {
+    static_assert(BYTES >= 40 * 256, "scratch");
+    attn_finish<D, BM, 256>(p, it, tid, reinterpret_cast<float *>(lds), [&](int u, AttnSums &out) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            out[e] = f[u][e];
-        mm = fm[u];
-        ll = fl[u];
+            out.f[e] = f[u][e];
+        out.m = fm[u];
+        out.l = fl[u];
     });
 }
 
@@ -1289,15 +1362,16 @@ void mx_attn_tile(AttnArgs p)
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<v4f *>(mine + 32 * d + 8 * i) = v4f{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
     __syncthreads();
-    attn_finish<D, BM, THR>(p, it, tid, [&](int u, float (&f)[8], float &mm, float &ll) {
+    static_assert(BYTES >= 40 * THR, "scratch");
+    attn_finish<D, BM, THR>(p, it, tid, reinterpret_cast<float *>(lds), [&](int u, AttnSums &out) {
         constexpr int RUNS = D / 8;
         const int i = tid + THR * u, n = i / RUNS;
         const float *src = reinterpret_cast<const float *>(lds) + n * OROW + i % RUNS * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            f[e] = src[e];
-        mm = ml[n][0];
-        ll = ml[n][1];
+            out.f[e] = src[e];
+        out.m = ml[n][0];
+        out.l = ml[n][1];
     });
 }
 

@@ -191,8 +191,10 @@ AttnFn attn_fn(int which)
 template <int F, int D>
 AttnFn attn_fn(int which, int64_t page_size)
 {
-    // a wave's load instruction covers 64 chunks of 16 bytes
-    return page_size >= 64 / AttnGeom<F, D>::CH ? attn_fn<F, D, 1>(which) : attn_fn<F, D, 0>(which);
+    // mx_attn_rows takes tiles of two pages, mx_attn_tile loads of one wave
+    // (64 chunks of 16 bytes)
+    const bool paged = page_size >= (which <= ROWS_32 ? 16 : 64 / AttnGeom<F, D>::CH);
+    return paged ? attn_fn<F, D, 1>(which) : attn_fn<F, D, 0>(which);
 }
 
 AttnFn attn_fn(int which, bool fp4, int64_t dim, int64_t page_size)
