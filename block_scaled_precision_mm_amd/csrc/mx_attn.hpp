@@ -126,6 +126,12 @@ __device__ __forceinline__ T wave_prefix(T v)
 
 __device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
+// v of the lane before; `first` in lane 0.
+__device__ __forceinline__ int lane_before(int v, int first)
+{
+    return __builtin_amdgcn_update_dpp(first, v, 0x138, 0xF, 0xF, false);
+}
+
 // A sequence as a lane sees it: row tiles and key tiles of the sequences of
 // this launch's class, 0 row tiles for others.
 struct AttnSeq {
@@ -146,16 +152,14 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &p, int s, int &carry
         end = min(max(p.ends[s], carry), p.tokens);
         q.len = min(max(p.lens[s], 0), p.table_width << p.page_shift);
     }
-    int before = __shfl_up(end, 1);
-    before = lane ? before : carry;
+    int before = lane_before(end, carry);
     if (__any(mine && end < before)) {
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
             const int u = __shfl_up(end, d);
             end = lane >= d ? max(end, u) : end;
         }
-        before = __shfl_up(end, 1);
-        before = lane ? before : carry;
+        before = lane_before(end, carry);
     }
     carry = lane_value(end, 63);
     q.tok0 = before;
@@ -195,7 +199,9 @@ __device__ __forceinline__ bool plan_item(const AttnArgs &p, int min_tiles, Attn
             const AttnSeq r = attn_seq<BM, BN>(p, s0 + lane, carry);
             total += (float)r.rtiles * (float)r.ktiles;
         }
-        total = __int_as_float(lane_value(__float_as_int(wave_prefix(total)), 63)) * p.per_target * 1.001f;
+        if (p.seqs > 1)
+            total = wave_prefix(total);
+        total = __int_as_float(lane_value(__float_as_int(total), p.seqs > 1 ? 63 : 0)) * p.per_target * 1.001f;
         chunk = max(uniform((int)fminf(total, 1e9f) + 1), min_tiles);
     }
     carry = carry64;
@@ -207,10 +213,19 @@ __device__ __forceinline__ bool plan_item(const AttnArgs &p, int min_tiles, Attn
             q = attn_seq<BM, BN>(p, s0 + lane, carry);
         const int parts = max(1, cdiv_u(q.ktiles, chunk));
         const int mytiles = p.heads * q.rtiles, mine = mytiles * parts;
-        const int upto = wave_prefix(mine), slots_upto = wave_prefix(parts > 1 ? mine : 0), tiles_upto = wave_prefix(mytiles);
-        const int all = lane_value(upto, 63);
+        int upto = mine, slots_upto = parts > 1 ? mine : 0, tiles_upto = mytiles;
+        if (p.seqs > 1) {
+            upto = wave_prefix(upto);
+            if (p.counters) {
+                slots_upto = wave_prefix(slots_upto);
+                tiles_upto = wave_prefix(tiles_upto);
+            }
+        }
+        const int all = lane_value(upto, p.seqs > 1 ? 63 : 0);
         if (item >= all) {
             item -= all;
+            if (p.seqs == 1)
+                return false;
             slots += lane_value(slots_upto, 63);
             tiles += lane_value(tiles_upto, 63);
             continue;
@@ -640,7 +655,7 @@ void mx_attn_rows(AttnArgs p)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g = lane >> 4;
 
     AttnItem it;
-    if (!plan_item<BM, BN>(p, 1, it))
+    if (!plan_item<BM, BN>(p, 2, it))
         return;
 
     const int *table = p.table + it.seq * p.table_stride;
@@ -799,8 +814,13 @@ void mx_attn_rows(AttnArgs p)
                 }
                 return sum;
             };
-            float sum = weights(m[t]);
-            if (__builtin_expect(__any(!(sum <= kMostSum)), 0)) {
+            float sum = 0.0f;
+            bool raise = key < it.key0 + BN;        // the wave's first tile
+            if (!raise) {
+                sum = weights(m[t]);
+                raise = __any(!(sum <= kMostSum));
+            }
+            if (__builtin_expect(raise, 0)) {
                 float top = -__builtin_inff();
 #pragma unroll
                 for (int e = 0; e < 8; ++e)

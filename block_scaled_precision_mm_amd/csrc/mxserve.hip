@@ -174,8 +174,19 @@ typedef void (*AttnFn)(AttnArgs);
 enum { ROWS_16 = 0, ROWS_32 = 1, ROWS_128 = 2, ROWS_256 = 3 };
 constexpr int kAttnBM[4] = {16, 32, 128, 256};
 constexpr int kAttnThreads[4] = {256, 256, 256, 512};
-// workgroups that run at once on 256 CUs
-constexpr int kAttnTarget[4] = {768, 512, 512, 256};
+// Parts that the key tiles are cut into: about as many as run at once on 256
+// CUs.  (mx_attn_rows: with few row tiles each has many parts, whose join
+// costs: one sequence of 100000 keys 47 us cut into 512 parts, 54 into 1024.
+// With a row tile per workgroup slot or more they balance ragged lengths: 64
+// sequences of 100 to 16000 keys 100 and 95 us.)
+int attn_target(int which, int64_t row_tiles)
+{
+    switch (which) {
+    case ROWS_16: return row_tiles < 512 ? 512 : 1024;
+    case ROWS_256: return 256;
+    default: return 512;
+    }
+}
 
 template <int F, int D, int PAGED>
 AttnFn attn_fn(int which)
@@ -211,6 +222,7 @@ struct AttnPlan {
     int which[2];
     int above[2], upto[2];
     int64_t base[2];        // most row tiles
+    int target[2];          // parts
     size_t bytes[2];        // of the workspace for splitting; 0: none
 };
 
@@ -234,10 +246,11 @@ AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
         p.upto[1] = 32;
     }
     for (int i = 0; i < p.n; ++i) {
-        const int bm = kAttnBM[p.which[i]], target = kAttnTarget[p.which[i]];
+        const int bm = kAttnBM[p.which[i]];
         const int64_t some = std::min(seqs, tokens);        // sequences with a new token
         p.base[i] = heads * (p.upto[i] <= bm ? some : tokens * group / bm + some);
-        p.bytes[i] = p.base[i] <= kSplitCounters ? (size_t)2 * target * attn_slot_bytes(bm, (int)dim) : 0;
+        p.target[i] = attn_target(p.which[i], p.base[i]);
+        p.bytes[i] = p.base[i] <= kSplitCounters ? (size_t)2 * p.target[i] * attn_slot_bytes(bm, (int)dim) : 0;
     }
     return p;
 }
@@ -351,8 +364,8 @@ int mx_paged_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_str
         a.parts = parts ? (uint8_t *)workspace + kSplitCounters * sizeof(unsigned) : nullptr;
         a.rows_above = plan.above[i];
         a.rows_upto = plan.upto[i];
-        a.per_target = (float)a.heads / (float)kAttnTarget[which];
-        const int64_t grid = plan.base[i] + (parts ? kAttnTarget[which] : 0);
+        a.per_target = (float)a.heads / (float)plan.target[i];
+        const int64_t grid = plan.base[i] + (parts ? plan.target[i] : 0);
         if (grid > INT32_MAX)
             return MXG_ERR_SHAPE;
         hipLaunchKernelGGL(attn_fn(which, cache->is_fp4 != 0, cache->head_dim, cache->page_size), dim3((unsigned)grid),
