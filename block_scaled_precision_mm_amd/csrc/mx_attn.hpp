@@ -39,9 +39,9 @@
 // has as many workgroups as can run at once plus one per (sequence, head,
 // row tile); each finds its own item from the lengths: key ranges longer
 // than the average work per resident workgroup are split, and the parts of
-// one row tile joined through a workspace by the workgroup that arrives
-// last, in part order (as mx_splitk.hpp does), so results do not depend on
-// timing.
+// one row tile joined through a workspace, by the workgroup that arrives
+// last (few rows) or by a second kernel (many rows), in a fixed order, so
+// results do not depend on timing.
 //
 // Masked places.  Scores of unseen keys are replaced, never added to;
 // values of slots past the sequence's end or on pages outside the cache are
@@ -176,9 +176,11 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &p, int s, int &carry
 
 __device__ __forceinline__ int cdiv_u(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1u) / (unsigned)b); }
 
-// Find workgroup `blockIdx.x`'s item; false if it has none.  Every wave of
-// the workgroup computes it (all results are wave-uniform).  min_tiles: the
-// fewest key tiles worth a part of their own.
+// Find item `item` of the launch; false if there is none.  Every wave of the
+// workgroup computes it (all results are wave-uniform).  min_tiles: the
+// fewest key tiles worth a part of their own.  JOIN: one item per row tile
+// of more than one part (at most as many as there are workgroups to run at
+// once), instead of one per part.
 //
 // A sequence's key tiles are cut into parts of at most `chunk`, where chunk
 // is at least the total of (row tile, key tile) pairs over the number of
@@ -186,8 +188,8 @@ __device__ __forceinline__ int cdiv_u(int a, int b) { return (int)(((unsigned)a 
 // twice that number of parts in all, which bounds the workspace, and the
 // items are at most one per row tile and that number more, which bounds the
 // grid (the factor keeps both with the FP32 total's rounding).
-template <int BM, int BN>
-__device__ __forceinline__ bool plan_item(const AttnArgs &p, int min_tiles, AttnItem &it)
+template <int BM, int BN, int JOIN = 0>
+__device__ __forceinline__ bool plan_item(const AttnArgs &p, int item, int min_tiles, AttnItem &it)
 {
     const int lane = threadIdx.x & 63;
     int chunk = 1 << 30, carry = 0;
@@ -205,15 +207,15 @@ __device__ __forceinline__ bool plan_item(const AttnArgs &p, int min_tiles, Attn
         chunk = max(uniform((int)fminf(total, 1e9f) + 1), min_tiles);
     }
     carry = carry64;
-    int item = blockIdx.x, slots = 0, tiles = 0;      // before the 64 sequences looked at
+    int slots = 0, tiles = 0;                         // before the 64 sequences looked at
     for (int s0 = 0;; s0 += 64) {
         if (s0 >= p.seqs)
             return false;
         if (s0 > 0)
             q = attn_seq<BM, BN>(p, s0 + lane, carry);
         const int parts = max(1, cdiv_u(q.ktiles, chunk));
-        const int mytiles = p.heads * q.rtiles, mine = mytiles * parts;
-        int upto = mine, slots_upto = parts > 1 ? mine : 0, tiles_upto = mytiles;
+        const int mytiles = p.heads * q.rtiles, myparts = mytiles * parts, mine = !JOIN ? myparts : parts > 1 ? mytiles : 0;
+        int upto = mine, slots_upto = parts > 1 ? myparts : 0, tiles_upto = mytiles;
         if (p.seqs > 1) {
             upto = wave_prefix(upto);
             if (p.counters) {
@@ -237,7 +239,7 @@ __device__ __forceinline__ bool plan_item(const AttnArgs &p, int min_tiles, Attn
         it.len = lane_value(q.len, at);
         const int rtiles = lane_value(q.rtiles, at), sparts = lane_value(parts, at), smine = lane_value(mine, at);
         item -= lane_value(upto, at) - smine;
-        slots += lane_value(slots_upto, at) - (sparts > 1 ? smine : 0);
+        slots += lane_value(slots_upto, at) - (sparts > 1 ? lane_value(myparts, at) : 0);
         tiles += lane_value(tiles_upto, at) - p.heads * rtiles;
         // heads innermost: the workgroups of a head, which share its keys,
         // are then apart by the number of heads and (with 8) on one XCD
@@ -485,65 +487,106 @@ struct AttnSums {
     }
 };
 
-// The end of a row tile.  Its sums lie with the threads of the workgroup as
-// runs of eight columns: run u of thread `tid` is columns 8 (i % (D / 8)) ..
-// + 7 of row i / (D / 8), i = tid + u * NTHR, for the rows that are there.
-// get(u, sums): the run's sums.  Writes outputs and lse, or for a split row
-// tile the part, and the whole in the workgroup that arrives last.
+// Run i of a row tile (columns 8 (i % (D / 8)) .. + 7 of row i / (D / 8)):
+// outputs and lse.
+template <int D>
+__device__ __forceinline__ void attn_write(const AttnArgs &p, const AttnItem &it, int i, AttnSums &s)
+{
+    constexpr int RUNS = D / 8;
+    const int run = i % RUNS;
+    const AttnRow r = attn_row(p, it, it.row0 + i / RUNS);
+    const size_t row = (size_t)(it.tok0 + r.token) * (p.heads * p.group) + it.head * p.group + r.head;
+    // (a row that sees no key has l = 0 and sums 0; a NaN is not 0)
+    const float inv = s.l == 0.0f ? 0.0f : 1.0f / s.l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        s.f[e] *= inv;
+    attn_store8(p, row, D, 8 * run, s.f);
+    if (p.lse && run == 0)
+        p.lse[row] = s.l == 0.0f ? -__builtin_inff() : (s.m + __builtin_amdgcn_logf(s.l)) * 0.6931471805599453f;
+}
+
+constexpr int kDeviceScope = 16;    // cache policy of a device-scope access
+
+// The workspace slot of a part.
+template <int D, int NR>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t attn_slot(const AttnArgs &p, const AttnItem &it, int part)
+{
+    constexpr int SLOT = attn_slot_bytes(NR, D);
+    return make_rsrc(p.parts + (size_t)(it.slot + part * it.slot_step) * SLOT, (unsigned)SLOT);
+}
+
+// Run i of this part into its slot.
+template <int D, int NR>
+__device__ __forceinline__ void attn_put_part(__amdgpu_buffer_rsrc_t slot, int i, const AttnSums &s)
+{
+    constexpr int RUNS = D / 8, SUMS = NR * D * 4;
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v4f{s.f[0], s.f[1], s.f[2], s.f[3]}), slot,
+                                           (unsigned)(i * 32), 0, kDeviceScope);
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v4f{s.f[4], s.f[5], s.f[6], s.f[7]}), slot,
+                                           (unsigned)(i * 32 + 16), 0, kDeviceScope);
+    if (i % RUNS == 0)
+        __builtin_amdgcn_raw_buffer_store_b64(u2v{__float_as_uint(s.m), __float_as_uint(s.l)}, slot,
+                                              (unsigned)(SUMS + i / RUNS * 8), 0, kDeviceScope);
+}
+
+// Parts first, first + step, .. of run i, in that order.
+template <int D, int NR>
+__device__ __forceinline__ void attn_sum_parts(const AttnArgs &p, const AttnItem &it, int i, int first, int step, AttnSums &s)
+{
+    constexpr int RUNS = D / 8, SUMS = NR * D * 4;
+    s.clear();
+    constexpr int PF = 8;       // parts in flight
+    for (int q0 = first; q0 < it.parts; q0 += PF * step) {
+        u4v a[PF], b[PF];
+        u2v ml[PF];
+#pragma unroll
+        for (int q = 0; q < PF; ++q) {
+            const __amdgpu_buffer_rsrc_t src = attn_slot<D, NR>(p, it, min(q0 + q * step, it.parts - 1));
+            ml[q] = __builtin_amdgcn_raw_buffer_load_b64(src, (unsigned)(SUMS + i / RUNS * 8), 0, kDeviceScope);
+            a[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(i * 32), 0, kDeviceScope);
+            b[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(i * 32 + 16), 0, kDeviceScope);
+        }
+#pragma unroll
+        for (int q = 0; q < PF; ++q)
+            if (q0 + q * step < it.parts) {
+                const v4f fa = __builtin_bit_cast(v4f, a[q]), fb = __builtin_bit_cast(v4f, b[q]);
+                s.add({fa[0], fa[1], fa[2], fa[3], fb[0], fb[1], fb[2], fb[3]}, __uint_as_float(ml[q][0]),
+                      __uint_as_float(ml[q][1]));
+            }
+    }
+}
+
+// The end of a part of a row tile of few rows, of which run u of thread `tid`
+// (i = tid + u NTHR, for the rows that are there) has the sums get(u, sums):
+// the outputs, or where the row tile is split the part, and the whole in the
+// workgroup that arrives last.
 //
-// That workgroup reads parts * rows * D sums alone, one memory latency after
-// the other, which for one sequence's few rows cost more than the keys (4
-// rows of 64 parts 30 of 64 us): so parts hold only the rows that are there,
-// and where these leave threads over, two or four groups of threads take
-// every second or fourth part each and are joined in `scratch` (of 40 NTHR
-// bytes of LDS that nothing else uses any more).
+// That workgroup reads the parts alone, one memory latency after the other,
+// which for one sequence's few rows cost more than the keys (4 rows of 64
+// parts 30 of 64 us): so parts hold only the rows that are there, and where
+// these leave threads over, two or four groups of threads take every second
+// or fourth part each and are joined in `scratch` (40 NTHR bytes of LDS that
+// nothing else uses any more).
 template <int D, int NR, int NTHR, class Get>
 __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &it, int tid, float *scratch, Get &&get)
 {
     constexpr int RUNS = D / 8, NU = cdiv_c(NR * RUNS, NTHR);
-    const int nrows = min(NR, it.ntok * p.group - it.row0), n = nrows * RUNS;
-    auto write = [&](int i, AttnSums &s) {
-        const int run = i % RUNS;
-        const AttnRow r = attn_row(p, it, it.row0 + i / RUNS);
-        const size_t row = (size_t)(it.tok0 + r.token) * (p.heads * p.group) + it.head * p.group + r.head;
-        // (a row that sees no key has l = 0 and sums 0; a NaN is not 0)
-        const float inv = s.l == 0.0f ? 0.0f : 1.0f / s.l;
+    const int n = min(NR, it.ntok * p.group - it.row0) * RUNS;
+    const __amdgpu_buffer_rsrc_t slot = attn_slot<D, NR>(p, it, it.part);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            s.f[e] *= inv;
-        attn_store8(p, row, D, 8 * run, s.f);
-        if (p.lse && run == 0)
-            p.lse[row] = s.l == 0.0f ? -__builtin_inff() : (s.m + __builtin_amdgcn_logf(s.l)) * 0.6931471805599453f;
-    };
-    if (it.parts == 1) {
-#pragma unroll
-        for (int u = 0; u < NU; ++u)
-            if (tid + u * NTHR < n) {
-                AttnSums s;
-                get(u, s);
-                write(tid + u * NTHR, s);
-            }
+    for (int u = 0; u < NU; ++u)
+        if (tid + u * NTHR < n) {
+            AttnSums s;
+            get(u, s);
+            if (it.parts == 1)
+                attn_write<D>(p, it, tid + u * NTHR, s);
+            else
+                attn_put_part<D, NR>(slot, tid + u * NTHR, s);
+        }
+    if (it.parts == 1)
         return;
-    }
-    constexpr int SUMS = NR * D * 4, SLOT = attn_slot_bytes(NR, D), DEV = 16;
     __shared__ unsigned arrived;
-    const __amdgpu_buffer_rsrc_t mine =
-        make_rsrc(p.parts + (size_t)(it.slot + it.part * it.slot_step) * SLOT, (unsigned)SLOT);
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-        const int i = tid + u * NTHR;
-        if (i >= n)
-            continue;
-        AttnSums s;
-        get(u, s);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v4f{s.f[0], s.f[1], s.f[2], s.f[3]}), mine,
-                                               (unsigned)(i * 32), 0, DEV);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v4f{s.f[4], s.f[5], s.f[6], s.f[7]}), mine,
-                                               (unsigned)(i * 32 + 16), 0, DEV);
-        if (i % RUNS == 0)
-            __builtin_amdgcn_raw_buffer_store_b64(u2v{__float_as_uint(s.m), __float_as_uint(s.l)}, mine,
-                                                  (unsigned)(SUMS + i / RUNS * 8), 0, DEV);
-    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (tid == 0)
@@ -551,38 +594,13 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
     __syncthreads();
     if (arrived != (unsigned)(it.parts - 1))
         return;
-    // parts first, first + step, .. of run i
-    auto sum_parts = [&](int i, int first, int step, AttnSums &s) {
-        s.clear();
-        constexpr int PF = 8;       // parts in flight
-        for (int q0 = first; q0 < it.parts; q0 += PF * step) {
-            u4v a[PF], b[PF];
-            u2v ml[PF];
-#pragma unroll
-            for (int q = 0; q < PF; ++q) {
-                const int part = min(q0 + q * step, it.parts - 1);
-                const __amdgpu_buffer_rsrc_t src =
-                    make_rsrc(p.parts + (size_t)(it.slot + part * it.slot_step) * SLOT, (unsigned)SLOT);
-                ml[q] = __builtin_amdgcn_raw_buffer_load_b64(src, (unsigned)(SUMS + i / RUNS * 8), 0, DEV);
-                a[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(i * 32), 0, DEV);
-                b[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(i * 32 + 16), 0, DEV);
-            }
-#pragma unroll
-            for (int q = 0; q < PF; ++q)
-                if (q0 + q * step < it.parts) {
-                    const v4f fa = __builtin_bit_cast(v4f, a[q]), fb = __builtin_bit_cast(v4f, b[q]);
-                    s.add({fa[0], fa[1], fa[2], fa[3], fb[0], fb[1], fb[2], fb[3]}, __uint_as_float(ml[q][0]),
-                          __uint_as_float(ml[q][1]));
-                }
-        }
-    };
     const int groups = n <= NTHR / 4 ? 4 : n <= NTHR / 2 ? 2 : 1;
     if (groups > 1) {
         // (whole waves per group: `first` is a scalar)
         const int each = NTHR / groups, group = uniform(tid / each), i = tid - group * each;
         AttnSums s;
         if (i < n) {
-            sum_parts(i, group, groups, s);
+            attn_sum_parts<D, NR>(p, it, i, group, groups, s);
             if (group > 0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -598,18 +616,47 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
                 s.add({src[0], src[NTHR], src[2 * NTHR], src[3 * NTHR], src[4 * NTHR], src[5 * NTHR], src[6 * NTHR], src[7 * NTHR]},
                       src[8 * NTHR], src[9 * NTHR]);
             }
-            write(i, s);
+            attn_write<D>(p, it, i, s);
         }
     } else {
 #pragma unroll 1
         for (int i = tid; i < n; i += NTHR) {
             AttnSums s;
-            sum_parts(i, 0, 1, s);
-            write(i, s);
+            attn_sum_parts<D, NR>(p, it, i, 0, 1, s);
+            attn_write<D>(p, it, i, s);
         }
     }
     if (tid == 0)
         __hip_atomic_store(p.counters + it.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Key tiles worth a part of their own in mx_attn_tile (16 tokens of 4 heads a
+// group over 8000 keys: 2 tiles 34 us, 4 27 us, 8 25 us).
+constexpr int kTileParts = 8;
+
+// The join of row tiles of many rows, a kernel of its own behind mx_attn_tile:
+// 512 runs of a row tile per workgroup.  (The last workgroup of a row tile,
+// joining alone as above, took 30 us for 31 parts of 64 rows.)
+constexpr int attn_join_blocks(int rows, int dim) { return cdiv_c(rows * dim / 8, 512); }
+
+template <int D, int BM>
+__global__ __launch_bounds__(256)
+void mx_attn_join(AttnArgs p)
+{
+    constexpr int RUNS = D / 8, SUB = attn_join_blocks(BM, D);
+    AttnItem it;
+    if (!plan_item<BM, 64, 1>(p, blockIdx.x / SUB, kTileParts, it) || it.parts == 1)
+        return;
+    const int n = min(BM, it.ntok * p.group - it.row0) * RUNS;
+#pragma unroll 1
+    for (int u = 0; u < 2; ++u) {
+        const int i = (blockIdx.x % SUB * 2 + u) * 256 + threadIdx.x;
+        if (i < n) {
+            AttnSums s;
+            attn_sum_parts<D, BM>(p, it, i, 0, 1, s);
+            attn_write<D>(p, it, i, s);
+        }
+    }
 }
 
 // ------------------------------------------------------------ few rows
@@ -655,7 +702,7 @@ void mx_attn_rows(AttnArgs p)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g = lane >> 4;
 
     AttnItem it;
-    if (!plan_item<BM, BN>(p, 2, it))
+    if (!plan_item<BM, BN>(p, blockIdx.x, 2, it))
         return;
 
     const int *table = p.table + it.seq * p.table_stride;
@@ -1014,7 +1061,7 @@ void mx_attn_tile(AttnArgs p)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 31, h = lane >> 5;
 
     AttnItem it;
-    if (!plan_item<BM, BN>(p, 4, it))
+    if (!plan_item<BM, BN>(p, blockIdx.x, kTileParts, it))
         return;
 
     const int *table = p.table + it.seq * p.table_stride;
@@ -1382,17 +1429,23 @@ void mx_attn_tile(AttnArgs p)
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<v4f *>(mine + 32 * d + 8 * i) = v4f{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
     __syncthreads();
-    static_assert(BYTES >= 40 * THR, "scratch");
-    attn_finish<D, BM, THR>(p, it, tid, reinterpret_cast<float *>(lds), [&](int u, AttnSums &out) {
-        constexpr int RUNS = D / 8;
-        const int i = tid + THR * u, n = i / RUNS;
-        const float *src = reinterpret_cast<const float *>(lds) + n * OROW + i % RUNS * 8;
+    constexpr int RUNS = D / 8;
+    const int n = min(BM, it.ntok * p.group - it.row0) * RUNS;
+    const __amdgpu_buffer_rsrc_t slot = attn_slot<D, BM>(p, it, it.part);
+    for (int i = tid; i < n; i += THR) {
+        const int rr = i / RUNS;
+        const float *src = reinterpret_cast<const float *>(lds) + rr * OROW + i % RUNS * 8;
+        AttnSums s;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            out.f[e] = src[e];
-        out.m = ml[n][0];
-        out.l = ml[n][1];
-    });
+            s.f[e] = src[e];
+        s.m = ml[rr][0];
+        s.l = ml[rr][1];
+        if (it.parts == 1)
+            attn_write<D>(p, it, i, s);
+        else
+            attn_put_part<D, BM>(slot, i, s);
+    }
 }
 
 }  // namespace mxg

@@ -47,27 +47,39 @@ __device__ __forceinline__ long long cache_at(const CacheArgs &p, long long slot
     return (((page * p.heads + head) << p.page_shift) + off) * p.dim + 8 * piece;
 }
 
+// U pieces per thread, all their loads in flight together.
+constexpr int kCachePieces = 4;
+
 template <int F>
 __global__ __launch_bounds__(256)
 void mx_cache_write(CacheArgs p)
 {
-    const int kv = blockIdx.y;
-    constexpr int U = 2;
+    constexpr int U = kCachePieces;
+    const int kv = blockIdx.y, first = (int)blockIdx.x * U * 256 + (int)threadIdx.x;
+    long long slot[U];
+    u4v w[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int i = ((int)blockIdx.x * U + u) * 256 + (int)threadIdx.x;
-        if (i >= p.n)
-            return;
-        const int t = p.per_token.div(i), in_token = i - t * (int)p.per_token.d;
-        const long long slot = p.slots[t];
-        const u4v w = __builtin_nontemporal_load(
-            reinterpret_cast<const u4v *>(p.in[kv] + t * p.stride[kv] + 8 * in_token));
-        const unsigned s = mx_scale_code<F>(quad_max(amax8(w)));
-        const u2v c = mx_encode8<F>(w, s);
-        if (slot < 0 || slot >= p.nslots)
+        const int i = first + u * 256;
+        slot[u] = -1;
+        w[u] = u4v{0u, 0u, 0u, 0u};
+        if (i < p.n) {
+            const int t = p.per_token.div(i);
+            slot[u] = p.slots[t];
+            w[u] = __builtin_nontemporal_load(
+                reinterpret_cast<const u4v *>(p.in[kv] + t * p.stride[kv] + 8 * (i - t * (int)p.per_token.d)));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = first + u * 256;
+        const unsigned s = mx_scale_code<F>(quad_max(amax8(w[u])));
+        const u2v c = mx_encode8<F>(w[u], s);
+        if (slot[u] < 0 || slot[u] >= p.nslots)
             continue;
+        const int in_token = i - p.per_token.div(i) * (int)p.per_token.d;
         const int head = p.per_head.div(in_token), piece = in_token - head * (int)p.per_head.d;
-        const long long at = cache_at(p, slot, head, piece);
+        const long long at = cache_at(p, slot[u], head, piece);
         if constexpr (F == FMT_FP4)
             *reinterpret_cast<unsigned *>(p.codes[kv] + (at >> 1)) = c[0];
         else
@@ -106,27 +118,37 @@ template <int F>
 __global__ __launch_bounds__(256)
 void mx_cache_read(CacheArgs p)
 {
-    const int kv = blockIdx.y;
-    constexpr int U = 2;
+    constexpr int U = kCachePieces;
+    const int kv = blockIdx.y, first = (int)blockIdx.x * U * 256 + (int)threadIdx.x;
+    u2v c[U];
+    unsigned s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int i = ((int)blockIdx.x * U + u) * 256 + (int)threadIdx.x;
-        if (i >= p.n)
-            return;
-        const int t = p.per_token.div(i), in_token = i - t * (int)p.per_token.d;
-        const long long slot = p.slots[t];
-        u4v w = {0u, 0u, 0u, 0u};
-        if (slot >= 0 && slot < p.nslots) {
-            const int head = p.per_head.div(in_token), piece = in_token - head * (int)p.per_head.d;
-            const long long at = cache_at(p, slot, head, piece);
-            u2v c = {0u, 0u};
-            if constexpr (F == FMT_FP4)
-                c[0] = *reinterpret_cast<const unsigned *>(p.codes[kv] + (at >> 1));
-            else
-                c = *reinterpret_cast<const u2v *>(p.codes[kv] + at);
-            w = mx_decode8<F>(c, p.scales[kv][at >> 5]);
+        const int i = first + u * 256;
+        c[u] = u2v{0u, 0u};
+        s[u] = 127u;                    // a slot outside the cache reads zeros
+        if (i < p.n) {
+            const int t = p.per_token.div(i), in_token = i - t * (int)p.per_token.d;
+            const long long slot = p.slots[t];
+            if (slot >= 0 && slot < p.nslots) {
+                const int head = p.per_head.div(in_token), piece = in_token - head * (int)p.per_head.d;
+                const long long at = cache_at(p, slot, head, piece);
+                if constexpr (F == FMT_FP4)
+                    c[u][0] = *reinterpret_cast<const unsigned *>(p.codes[kv] + (at >> 1));
+                else
+                    c[u] = *reinterpret_cast<const u2v *>(p.codes[kv] + at);
+                s[u] = p.scales[kv][at >> 5];
+            }
         }
-        *reinterpret_cast<u4v *>(p.out[kv] + t * p.stride[kv] + 8 * in_token) = w;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = first + u * 256;
+        if (i < p.n) {
+            const int t = p.per_token.div(i), in_token = i - t * (int)p.per_token.d;
+            __builtin_nontemporal_store(mx_decode8<F>(c[u], s[u]),
+                                        reinterpret_cast<u4v *>(p.out[kv] + t * p.stride[kv] + 8 * in_token));
+        }
     }
 }
 
