@@ -520,12 +520,15 @@ def mx_noalloc_scratch_bytes() -> int:
 _BF16 = torch.bfloat16
 
 
-def _bf16_of(name, t, n):
-    """t: a contiguous bfloat16 CUDA tensor of n elements, a raw pointer or None."""
-    if t is None or t.__class__ is int:
-        return
+def _bf16_ptr(name, t, n):
+    """Address of a contiguous bfloat16 CUDA tensor of n elements, a raw pointer itself, 0 for None."""
+    if t is None:
+        return 0
+    if t.__class__ is int:
+        return t
     if t.dtype is not _BF16 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
         raise ValueError("%s must be a contiguous bfloat16 CUDA tensor of %d elements" % (name, n))
+    return t.data_ptr()
 
 
 def mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, stream=None) -> None:
@@ -535,13 +538,12 @@ def mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, 
     [rows][K] or E2M1 pairs [rows][K/2] with y_scale uint8 [rows][K/32]; a
     1-byte y takes its format from its size unless out_kind is given."""
     n = rows * K
-    _bf16_of("x", x, n)
-    _bf16_of("residual", residual, n)
-    _bf16_of("h", h, n)
-    _bf16_of("weight", weight, K)
+    px, pr, ph = _bf16_ptr("x", x, n), _bf16_ptr("residual", residual, n), _bf16_ptr("h", h, n)
+    pw = _bf16_ptr("weight", weight, K)
     if y.__class__ is int:
         if out_kind is None:
             raise ValueError("out_kind is required when y is a raw pointer")
+        py = y
     else:
         size = y.element_size()
         if out_kind is None:
@@ -551,12 +553,15 @@ def mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, 
         if not y.is_cuda or not y.is_contiguous() or size != (2, 2, 4, 1, 1)[out_kind] or \
                 y.numel() != (n // 2 if out_kind == OUT_MXFP4 else n):
             raise ValueError("y must be a contiguous CUDA tensor of rows*K values of its output kind")
-    if y_scale is not None and y_scale.__class__ is not int and (
-            not y_scale.is_cuda or not y_scale.is_contiguous() or y_scale.element_size() != 1 or
-            y_scale.numel() != rows * (K // 32)):
-        raise ValueError("y_scale must be a contiguous 1-byte CUDA tensor of rows*K/32 elements")
-    st = _lib.mx_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y), _ptr(y_scale), rows, K, eps,
-                         out_kind, _stream(stream))
+        py = y.data_ptr()
+    if y_scale is None or y_scale.__class__ is int:
+        ps = y_scale or 0
+    else:
+        if not y_scale.is_cuda or not y_scale.is_contiguous() or y_scale.element_size() != 1 or \
+                y_scale.numel() != rows * (K // 32):
+            raise ValueError("y_scale must be a contiguous 1-byte CUDA tensor of rows*K/32 elements")
+        ps = y_scale.data_ptr()
+    st = _lib.mx_rmsnorm(px, pr, pw, ph, py, ps, rows, K, eps, out_kind, _stream(stream))
     if st:
         raise MxGemmError(st, "mx_rmsnorm")
 
