@@ -13,7 +13,7 @@
 // E2M1 element times a power of two has at most 4 significant bits), both
 // products run on the BF16 MFMA with FP32 accumulation, q.k of the given BF16
 // q is exact but for the accumulation, x, m and the sums are FP32.  p is
-// rounded to BF16 as the second product's operand (half a step: 2^-9 of each
+// rounded to BF16 as the second product's operand (half a step: 2^-8 of each
 // p); the sum of the p's takes them unrounded.
 //
 // The rows of one KV head.  All G = q_heads / kv_heads query heads of a KV

@@ -142,7 +142,10 @@ void mx_rmsnorm_rows(NormArgs p)
         for (int i = 0; i < THR / 64; ++i)
             sum += part[i];
     }
-    const float r = (float)(1.0 / sqrt(sum / p.K + (double)p.eps));
+    // (1 / r beyond FP32's normal range: both factors of h * r moved into it)
+    const double rd = 1.0 / sqrt(sum / p.K + (double)p.eps);
+    const float move = rd < 0x1p-126 ? 0x1p-32f : rd > 0x1p127 ? 0x1p32f : 1.0f;
+    const float r = (float)(rd / move);
     const u4v *w = reinterpret_cast<const u4v *>(p.w);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -152,8 +155,8 @@ void mx_rmsnorm_rows(NormArgs p)
         float f[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            f[2 * i] = bf16_lo(v[j][i]) * r;
-            f[2 * i + 1] = bf16_hi(v[j][i]) * r;
+            f[2 * i] = bf16_lo(v[j][i]) * move * r;
+            f[2 * i + 1] = bf16_hi(v[j][i]) * move * r;
         }
         if (w) {
             const u4v g = w[at];

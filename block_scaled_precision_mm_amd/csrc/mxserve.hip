@@ -35,9 +35,15 @@ FastDiv fast_div(unsigned d)
 // Longest row: 1024 threads hold 64 values each.
 constexpr int64_t kMaxNormK = 65536;
 
+// A launch has fewer than 2^32 threads.
+constexpr int64_t kMaxThreads = UINT32_MAX;
+
 template <int THR, int NV>
-int launch_norm(const NormArgs &a, int64_t rows, int out_kind, hipStream_t stream)
+int launch_norm(NormArgs a, int64_t rows, int out_kind, hipStream_t stream)
 {
+    const bool fp4 = out_kind == MXG_OUT_MXFP4, mx = fp4 || out_kind == MXG_OUT_MXFP8;
+    const int64_t y_row = fp4 ? a.K / 2 : mx ? a.K : out_kind == MXG_OUT_F32 ? 4 * (int64_t)a.K : 2 * (int64_t)a.K;
+
     void (*fn)(NormArgs) = nullptr;
     switch (out_kind) {
     case MXG_OUT_BF16: fn = &mx_rmsnorm_rows<THR, NV, OUT_BF16>; break;
@@ -46,8 +52,22 @@ int launch_norm(const NormArgs &a, int64_t rows, int out_kind, hipStream_t strea
     case MXG_OUT_MXFP8: fn = &mx_rmsnorm_rows<THR, NV, OUT_MX8>; break;
     default: fn = &mx_rmsnorm_rows<THR, NV, OUT_MX4>; break;
     }
-    hipLaunchKernelGGL(fn, dim3((unsigned)rows), dim3(THR), 0, stream, a);
-    return host_hip_status(hipGetLastError());
+    for (;;) {
+        const int64_t n = std::min(rows, kMaxThreads / THR);
+        hipLaunchKernelGGL(fn, dim3((unsigned)n), dim3(THR), 0, stream, a);
+        const int rc = host_hip_status(hipGetLastError());
+        rows -= n;
+        if (rc || rows == 0)
+            return rc;
+        a.x += n * a.K;
+        if (a.res)
+            a.res += n * a.K;
+        if (a.h)
+            a.h += n * a.K;
+        a.y = (uint8_t *)a.y + n * y_row;
+        if (mx)
+            a.scales += n * (a.K / 32);
+    }
 }
 
 int run_norm(const void *x, const void *residual, const void *weight, void *h, void *y, void *y_scale,
@@ -339,11 +359,14 @@ int mx_paged_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_str
         return MXG_ERR_PTR_ALIGN;
     if (((uintptr_t)ends | (uintptr_t)lens | (uintptr_t)table | (uintptr_t)lse) & 3)
         return MXG_ERR_PTR_ALIGN;
+    const int64_t group = q_heads / cache->kv_heads;
+    const AttnPlan plan = attn_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new);
+    for (int i = 0; i < plan.n; ++i)        // (split ones are far below)
+        if (plan.base[i] > kMaxThreads / kAttnThreads[plan.which[i]])
+            return MXG_ERR_SHAPE;
     rc = host_check_device();
     if (rc || tokens == 0 || seqs == 0)
         return rc;
-    const int64_t group = q_heads / cache->kv_heads;
-    const AttnPlan plan = attn_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new);
     const bool split = workspace && workspace_bytes >= attn_workspace(plan);
     AttnArgs a;
     a.codes[0] = (const uint8_t *)cache->k_codes;
@@ -380,8 +403,6 @@ int mx_paged_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_str
         a.rows_upto = plan.upto[i];
         a.per_target = (float)a.heads / (float)plan.target[i];
         const int64_t grid = plan.base[i] + (parts ? plan.target[i] : 0);
-        if (grid > INT32_MAX)
-            return MXG_ERR_SHAPE;
         hipLaunchKernelGGL(attn_fn(which, cache->is_fp4 != 0, cache->head_dim, cache->page_size), dim3((unsigned)grid),
                            dim3(kAttnThreads[which]), 0, (hipStream_t)stream, a);
         rc = host_hip_status(hipGetLastError());

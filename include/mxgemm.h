@@ -356,12 +356,14 @@ int mx_dense_gemm(int dtype, int trans_a, int trans_b, const void *a, const void
  *              to BF16 and quantized exactly as mx_quantize_bf16 does, codes
  *              [rows][K] or [rows][K/2] into y and E8M0 codes [rows][K/32]
  *              into y_scale: the A operand of a following MX GEMM.
- * rows, K      rows >= 0 (0: nothing is enqueued, pointers may be NULL); K a positive multiple of
- *              32, at most 65536.
+ * rows, K      rows >= 0 (0: nothing is enqueued, pointers may be NULL); K a
+ *              positive multiple of 32, at most 65536.
  * eps          >= 0, finite.
  *
- * The sum of squares is taken in FP64.  A row that holds a NaN or an
- * infinity gives NaN (scale codes 0xFF), as the formula does.
+ * The sum of squares is taken in FP64.  A row that holds a NaN gives NaN; one
+ * that holds an infinity NaN in its place and 0 elsewhere, and a row of zeros
+ * with eps = 0 NaN, as the formula does (scale code 0xFF for a block with a
+ * NaN).
  * MXG_ERR_NULL, MXG_ERR_DTYPE (out_kind), MXG_ERR_SHAPE, MXG_ERR_K_ALIGN
  * (K % 32), MXG_ERR_CONFIG (eps), MXG_ERR_PTR_ALIGN (every pointer but
  * y_scale 16-byte aligned), MXG_ERR_DEVICE, MXG_ERR_HIP.
@@ -402,8 +404,8 @@ typedef struct {
  *            slot.  A slot outside the cache (-1, for padding) is skipped by
  *            a write and reads zeros.  Two tokens written to one slot leave
  *            either's values, block by block.
- * tokens     >= 0 (0: nothing is enqueued, k, v, slots may be NULL); tokens * kv_heads * head_dim
- *            at most 2^33.
+ * tokens     >= 0 (0: nothing is enqueued, k, v, slots may be NULL); tokens *
+ *            kv_heads * head_dim at most 2^33.
  *
  * MXG_ERR_NULL, MXG_ERR_SHAPE, MXG_ERR_K_ALIGN (head_dim % 32, a stride % 8),
  * MXG_ERR_PTR_ALIGN, MXG_ERR_DEVICE, MXG_ERR_HIP.
@@ -434,7 +436,7 @@ int mx_kv_cache_read(const mxg_kv_cache_t *cache, void *k, void *v, int64_t k_st
  *             sequence's keys are not looked at.
  * tokens      rows of q (and of out); q_heads a multiple of kv_heads.
  * max_new     the most new tokens of a sequence: chooses kernels, for speed
- *             only (any value gives the same results).
+ *             only (any value gives the same results but for rounding).
  * scale       > 0, finite (usually 1 / sqrt(head_dim)).
  * out         [tokens][q_heads][head_dim] of out_dtype (BF16, FP16, FP32),
  *             contiguous, 16-byte aligned.
@@ -457,7 +459,9 @@ int mx_kv_cache_read(const mxg_kv_cache_t *cache, void *k, void *v, int64_t k_st
  *
  * MXG_ERR_NULL, MXG_ERR_DTYPE (out_dtype), MXG_ERR_SHAPE (sizes; seqs or
  * q_heads above 65536; tokens * q_heads above 2^30; table_width * page_size
- * above 2^30; head_dim), MXG_ERR_K_ALIGN (head_dim % 32, q_stride % 8),
+ * above 2^30; head_dim; a launch of 2^24 row tiles or more, which
+ * kv_heads * (seqs + tokens * q_heads / kv_heads / 16) stays below in any
+ * sizes but the largest), MXG_ERR_K_ALIGN (head_dim % 32, q_stride % 8),
  * MXG_ERR_CONFIG (scale, causal), MXG_ERR_PTR_ALIGN, MXG_ERR_DEVICE,
  * MXG_ERR_HIP.
  */

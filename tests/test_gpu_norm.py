@@ -83,6 +83,28 @@ def test_zero_rows_and_extremes():
     _check(sr.bf16(x), None, None, 1e-30, "extremes, small eps")
 
 
+def test_norms_beyond_the_normal_range():
+    # 1 / norm is subnormal in FP32, or past its largest value
+    x = np.stack([np.linspace(1, 3.3, 256) * 1e38, np.linspace(-3, 3.05, 256) * 1.1e38, np.full(256, 2.0 ** -133),
+                  np.linspace(1, 120, 256).round() * 2.0 ** -133, np.linspace(-1, 1, 256)])
+    _check(sr.bf16(x), None, sr.bf16(np.linspace(-2, 2, 256)), 0.0, "beyond the normal range")
+
+
+def test_more_rows_than_a_launch_holds():
+    # 64 threads a row: 2^26 - 1 rows are a launch's most
+    rows, K = 2 ** 26 + 5, 32
+    x = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda").expand(rows, K).contiguous()
+    tail = torch.randn(16, K, device="cuda").bfloat16()
+    x[-16:] = tail
+    y = torch.empty(rows, K // 2, dtype=torch.uint8, device="cuda")
+    ys = torch.empty(rows, 1, dtype=torch.uint8, device="cuda")
+    mx.mx_rmsnorm(x, None, None, None, y, ys, rows, K, 0.0)
+    want, want_s, _ = mx.rmsnorm(tail, None, eps=0.0, out="fp4")
+    assert torch.equal(y[-16:], want) and torch.equal(ys[-16:].view(-1), want_s.view(-1))
+    one, one_s, _ = mx.rmsnorm(x[:1].contiguous(), None, eps=0.0, out="fp4")
+    assert bool((y[:-16] == one).all()) and bool((ys[:-16] == one_s.view(-1)).all())
+
+
 def test_nan_and_inf_rows_stay_apart():
     rng = np.random.default_rng(6)
     x = rng.standard_normal((5, 640))

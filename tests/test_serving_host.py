@@ -80,6 +80,7 @@ def test_attention_cache_refusals(kw, status):
     (dict(seqs=-1), -2), (dict(seqs=65537), -2), (dict(n=-1), -2), (dict(n=1 << 28), -2), (dict(heads=7), -2), (dict(heads=0), -2),
     (dict(heads=1), -2), (dict(most=-1), -2), (dict(width=-1), -2), (dict(width=1 << 27), -2), (dict(qst=1016), -2),
     (dict(qst=1 << 31), -2), (dict(window=-1), -2), (dict(c=cache(dim=96)), -2), (dict(c=cache(dim=256), qst=2048), -2),
+    (dict(c=cache(heads=256), qst=256 * 128, seqs=65536, n=65536, heads=256, most=1), -2),     # 2^24 row tiles and more
     (dict(q=0), -1), (dict(ends=0), -1), (dict(lens=0), -1), (dict(table=0), -1), (dict(out=0), -1),
     (dict(qst=1028), -3),
     (dict(scale=0.0), -9), (dict(scale=-1.0), -9), (dict(scale=float("nan")), -9), (dict(scale=float("inf")), -9), (dict(causal=2), -9),
