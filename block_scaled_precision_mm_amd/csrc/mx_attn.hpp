@@ -664,7 +664,11 @@ void mx_attn_join(AttnArgs p)
 // of 32 keys, each with its own sums, its own LDS and no barrier in the loop;
 // the sums are joined at the end.  Bound: HBM, the cache's bytes, and close
 // behind it (for MXFP4 codes before it) the VALU work of expanding them; the
-// next tile's codes are in flight while one is worked on.
+// next tile's codes are in flight while one is worked on.  64 sequences of 100
+// to 16000 keys, 8 KV heads of 128, E4M3: 436 MB in 93 us, 4.7 TB/s (a second
+// tile in flight 100 us: its registers cost a wave); three of 60000 to 131072
+// in E2M1: 349 MB in 69 us, 5.1 TB/s; one of 1025 keys 9.7 us: the launch, the
+// plan, a few dependent loads and the join.
 //
 // v_mfma_f32_16x16x32_bf16, lane (r = l & 15, g = l >> 4): operands row r,
 // k = 8g .. 8g + 7; accumulator column r, rows 4g .. 4g + 3.  So S^T tile kt
@@ -996,10 +1000,13 @@ __device__ __forceinline__ int value_swizzle(int key)
 //            fed from LDS, and between them expanding tile t + 1's codes
 //            into LDS and the loads of tile t + 2's
 //     V(t)   the softmax of tile t: VALU
-// Bound: MFMA, and beside it VALU issue.  With NW = 8 the two waves of a SIMD
-// are of different groups (waves 0-3 and 4-7): the one barrier per tile
-// stands behind V for the first and behind M for the second, so one's M runs
-// beside the other's V.  Between barriers t - 1 and t both groups are at
+// Bound: MFMA, and beside it VALU issue: 4096 tokens of 32 heads of 128 over
+// 8 KV heads behind 12204 keys in E4M3 (0.96 TFLOP) take 870 us, 1.1 PFLOP/s;
+// their MFMAs alone 526 us, with the LDS reads 575, with the softmax 785.
+//
+// With NW = 8 the two waves of a SIMD are of different groups (waves 0-3 and
+// 4-7): the one barrier per tile stands behind V for the first and behind M
+// for the second, so one's M runs beside the other's V.  Between barriers t - 1 and t both groups are at
 // M(t): they read keys t and values t - 1 and write tile t + 1, so two buffers
 // of keys and three of values keep them apart.  With NW = 4 (fewer rows to
 // waste, two workgroups per CU): a barrier behind each phase, the expansion

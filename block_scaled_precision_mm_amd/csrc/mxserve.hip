@@ -93,8 +93,13 @@ int run_norm(const void *x, const void *residual, const void *weight, void *h, v
         return rc;
     const NormArgs a = {(const uint16_t *)x, (const uint16_t *)residual, (const uint16_t *)weight,
                         (uint16_t *)h, y, (uint8_t *)y_scale, (int)K, eps};
-    // one workgroup per row: a wave up to 512 values, 256 threads up to 16384
-    // (at most eight 16-byte pieces each), 1024 beyond
+    // One workgroup per row, with up to four 16-byte pieces per thread (eight
+    // past 32768 values): a wave up to 512 values (16384 rows of them 14 us,
+    // with 256 threads 23), 256 threads up to 6144, 512 up to 16384 and 1024
+    // beyond.  Rows with residual and E4M3 output, 256 / 512 / 1024 threads:
+    // 8192 of 4096 values 41 / 47 / - us, of 5120 54 / 59 / 74, of 8192
+    // 79 / 79 / 98 (but 129 of them 6.0 / 4.9 / 4.9), 4096 of 16384
+    // 136 / 78 / 82.
     const int64_t pieces = K / 8;
     if (pieces <= 64)
         return launch_norm<64, 1>(a, rows, out_kind, stream);
@@ -102,9 +107,9 @@ int run_norm(const void *x, const void *residual, const void *weight, void *h, v
     case 1: return launch_norm<256, 1>(a, rows, out_kind, stream);
     case 2: return launch_norm<256, 2>(a, rows, out_kind, stream);
     case 3: return launch_norm<256, 3>(a, rows, out_kind, stream);
-    case 4: return launch_norm<256, 4>(a, rows, out_kind, stream);
-    case 5: case 6: return launch_norm<256, 6>(a, rows, out_kind, stream);
-    case 7: case 8: return launch_norm<256, 8>(a, rows, out_kind, stream);
+    case 4: return launch_norm<512, 2>(a, rows, out_kind, stream);
+    case 5: case 6: return launch_norm<512, 3>(a, rows, out_kind, stream);
+    case 7: case 8: return launch_norm<512, 4>(a, rows, out_kind, stream);
     }
     return pieces <= 4096 ? launch_norm<1024, 4>(a, rows, out_kind, stream)
                           : launch_norm<1024, 8>(a, rows, out_kind, stream);
@@ -196,13 +201,13 @@ constexpr int kAttnBM[4] = {16, 32, 128, 256};
 constexpr int kAttnThreads[4] = {256, 256, 256, 512};
 // Parts that the key tiles are cut into: about as many as run at once on 256
 // CUs.  (mx_attn_rows: with few row tiles each has many parts, whose join
-// costs: one sequence of 100000 keys 47 us cut into 512 parts, 54 into 1024.
-// With a row tile per workgroup slot or more they balance ragged lengths: 64
-// sequences of 100 to 16000 keys 100 and 95 us.)
-int attn_target(int which, int64_t row_tiles)
+// costs: one sequence of 100000 keys 47 us cut into 512 parts, 54 into 1024;
+// 32 sequences of 16 rows over 4096 keys 50 and 57.  With 512 row tiles they
+// balance ragged lengths: 64 sequences of 100 to 16000 keys 100 and 95 us.)
+int attn_target(int which, int64_t pairs)      // (sequence, head) pairs
 {
     switch (which) {
-    case ROWS_16: return row_tiles < 512 ? 512 : 1024;
+    case ROWS_16: return pairs < 512 ? 512 : 1024;
     case ROWS_128: return 384;
     case ROWS_256: return 256;
     default: return 512;
@@ -244,8 +249,15 @@ AttnFn attn_fn(int which, bool fp4, int64_t dim, int64_t page_size)
     return fp4 ? attn_fn<FMT_FP4, 128>(which, page_size) : attn_fn<FMT_FP8, 128>(which, page_size);
 }
 
+// Most rows (new tokens x heads of a group) of a sequence for mx_attn_rows,
+// which takes 32 at a time and so reads the keys of 64 twice, the second time
+// from a cache.  32 sequences of 64 rows over 4096 keys 66 us (MXFP4 54, 64-wide
+// heads 39), in tiles of 128 94 (86, 56), one over 8192 keys 26 and 30, 128
+// over 1024 keys 93 and 88; of 128 rows over 4096 keys 120 and 112.
+constexpr int kFewRows = 64;
+
 // What a call launches: one kernel for all sequences, or one for those of
-// few rows (new tokens x heads of a group) and one for the others.
+// few rows and one for the others.
 struct AttnPlan {
     int n;
     int which[2];
@@ -263,25 +275,25 @@ AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
     // a group behind 12204 keys 825 us against 935, 512 tokens 85 against 92),
     // else 128 (24 sequences of 1 to 600 tokens 52 us against 65)
     const int tile = tokens * group >= 512 * seqs ? ROWS_256 : ROWS_128;
-    if (most <= 32 || tokens == seqs * max_new) {
+    if (most <= kFewRows || tokens == seqs * max_new) {
         p.n = 1;
-        p.which[0] = most <= 16 ? ROWS_16 : most <= 32 ? ROWS_32 : tile;
+        p.which[0] = most <= 16 ? ROWS_16 : most <= kFewRows ? ROWS_32 : tile;
         p.above[0] = 0;
         p.upto[0] = INT32_MAX;
     } else {
         p.n = 2;
         p.which[0] = tile;
-        p.above[0] = 32;
+        p.above[0] = kFewRows;
         p.upto[0] = INT32_MAX;
         p.which[1] = ROWS_32;
         p.above[1] = 0;
-        p.upto[1] = 32;
+        p.upto[1] = kFewRows;
     }
     for (int i = 0; i < p.n; ++i) {
         const int bm = kAttnBM[p.which[i]];
         const int64_t some = std::min(seqs, tokens);        // sequences with a new token
-        p.base[i] = heads * (p.upto[i] <= bm ? some : tokens * group / bm + some);
-        p.target[i] = attn_target(p.which[i], p.base[i]);
+        p.base[i] = heads * std::min(tokens * group / bm + some, cdiv(p.upto[i], bm) * some);
+        p.target[i] = attn_target(p.which[i], heads * some);
         // (one sequence with a row tile per part or more is never split)
         const bool whole = seqs == 1 && heads * cdiv(tokens * group, bm) >= p.target[i];
         p.bytes[i] = p.base[i] <= kSplitCounters && !whole ? (size_t)2 * p.target[i] * attn_slot_bytes(bm, (int)dim) : 0;
