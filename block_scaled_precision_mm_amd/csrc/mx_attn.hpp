@@ -1001,16 +1001,17 @@ __device__ __forceinline__ int value_swizzle(int key)
 //            into LDS and the loads of tile t + 2's
 //     V(t)   the softmax of tile t: VALU
 // Bound: MFMA, and beside it VALU issue: 4096 tokens of 32 heads of 128 over
-// 8 KV heads behind 12204 keys in E4M3 (0.96 TFLOP) take 870 us, 1.1 PFLOP/s;
-// their MFMAs alone 526 us, with the LDS reads 575, with the softmax 785.
+// 8 KV heads behind 12204 keys in E4M3 (0.96 TFLOP) take 830 to 870 us, 1.1
+// PFLOP/s; their MFMAs alone 526 us, with the LDS reads 575, with the softmax 785.
 //
 // With NW = 8 the two waves of a SIMD are of different groups (waves 0-3 and
 // 4-7): the one barrier per tile stands behind V for the first and behind M
-// for the second, so one's M runs beside the other's V.  Between barriers t - 1 and t both groups are at
-// M(t): they read keys t and values t - 1 and write tile t + 1, so two buffers
-// of keys and three of values keep them apart.  With NW = 4 (fewer rows to
-// waste, two workgroups per CU): a barrier behind each phase, the expansion
-// and the loads in V, one buffer of keys and two of values.
+// for the second, so one's M runs beside the other's V.  Between barriers t -
+// 1 and t both groups are at M(t): they read keys t and values t - 1 and write
+// tile t + 1, so two buffers of keys and three of values keep them apart.
+// With NW = 4 (fewer rows to waste, two workgroups per CU): a barrier behind
+// each phase, the expansion and the loads in V, one buffer of keys and two of
+// values.
 //
 // v_mfma_f32_32x32x16_bf16, lane (r = l & 31, h = l >> 5): operands row r,
 // k = 8h .. 8h + 7; accumulator column r, register i row 8 (i >> 2) + 4h +
