@@ -630,8 +630,9 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
         __hip_atomic_store(p.counters + it.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Key tiles worth a part of their own in mx_attn_tile (16 tokens of 4 heads a
-// group over 8000 keys: 2 tiles 34 us, 4 27 us, 8 25 us).
+// Key tiles worth a part of their own in mx_attn_tile (64 rows over 8000 keys:
+// 2 tiles 34 us, 4 27, 8 25; 512 rows over 1500 keys: 8 tiles 32 us, 12 38,
+// 24 50).
 constexpr int kTileParts = 8;
 
 // The join of row tiles of many rows, a kernel of its own behind mx_attn_tile:

@@ -250,11 +250,22 @@ AttnFn attn_fn(int which, bool fp4, int64_t dim, int64_t page_size)
 }
 
 // Most rows (new tokens x heads of a group) of a sequence for mx_attn_rows,
-// which takes 32 at a time and so reads the keys of 64 twice, the second time
-// from a cache.  32 sequences of 64 rows over 4096 keys 66 us (MXFP4 54, 64-wide
-// heads 39), in tiles of 128 94 (86, 56), one over 8192 keys 26 and 30, 128
-// over 1024 keys 93 and 88; of 128 rows over 4096 keys 120 and 112.
-constexpr int kFewRows = 64;
+// which takes 32 at a time and so reads and expands a key once for each 32,
+// but cuts its keys finer and joins the parts itself, without a second
+// kernel.  That pays while there are few row tiles (8 KV heads of 128, E4M3):
+//     row tiles  sequences, rows, keys   us, in tiles of 128
+//          32    1 of 128 over 2048       16   27
+//         128    1 of 512 over 2048       22   33  (over 32768 keys 110 and 92)
+//         200    2 of 400 over 4096       46   41
+//         256    4 of 256 over 4096       40   43
+//         512    32 of 64 over 4096       66   94  (E2M1 54 and 86)
+//        1024    32 of 128 over 4096     120  112
+//        4096    128 of 128 over 1024    165  107
+// and for 64 rows, two row tiles, nearly always (2048: 93 and 88).
+int attn_few_rows(int64_t row_tiles)        // of 32 rows, all heads
+{
+    return row_tiles <= 128 ? 512 : row_tiles <= 256 ? 256 : 64;
+}
 
 // What a call launches: one kernel for all sequences, or one for those of
 // few rows and one for the others.
@@ -275,19 +286,20 @@ AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
     // a group behind 12204 keys 825 us against 935, 512 tokens 85 against 92),
     // else 128 (24 sequences of 1 to 600 tokens 52 us against 65)
     const int tile = tokens * group >= 512 * seqs ? ROWS_256 : ROWS_128;
-    if (most <= kFewRows || tokens == seqs * max_new) {
+    const int few = attn_few_rows(heads * cdiv(tokens * group, 32));
+    if (most <= few || tokens == seqs * max_new) {
         p.n = 1;
-        p.which[0] = most <= 16 ? ROWS_16 : most <= kFewRows ? ROWS_32 : tile;
+        p.which[0] = most <= 16 ? ROWS_16 : most <= few ? ROWS_32 : tile;
         p.above[0] = 0;
         p.upto[0] = INT32_MAX;
     } else {
         p.n = 2;
         p.which[0] = tile;
-        p.above[0] = kFewRows;
+        p.above[0] = few;
         p.upto[0] = INT32_MAX;
         p.which[1] = ROWS_32;
         p.above[1] = 0;
-        p.upto[1] = kFewRows;
+        p.upto[1] = few;
     }
     for (int i = 0; i < p.n; ++i) {
         const int bm = kAttnBM[p.which[i]];
