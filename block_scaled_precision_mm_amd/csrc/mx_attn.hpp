@@ -9,12 +9,13 @@
 // relative to a reference m, p_j = 2^(x_j log2 e - m).  A row that sees no key
 // gives 0 and lse = -inf.
 //
-// Types.  Codes are expanded to BF16 on the way into LDS (exactly: an E4M3 or
-// E2M1 element times a power of two has at most 4 significant bits), both
-// products run on the BF16 MFMA with FP32 accumulation, q.k of the given BF16
-// q is exact but for the accumulation, x, m and the sums are FP32.  p is
-// rounded to BF16 as the second product's operand (half a step: 2^-8 of each
-// p); the sum of the p's takes them unrounded.
+// Types.  Codes are expanded to BF16 on the way into LDS (exactly within its
+// range: an E4M3 or E2M1 element times a power of two has at most 4
+// significant bits), both products run on the BF16 MFMA with FP32
+// accumulation, q.k of the given BF16 q is exact but for the accumulation, x,
+// m and the sums are FP32.  p is rounded to BF16 as the second product's
+// operand (half a step: 2^-8 of each p); the sum of the p's takes them
+// unrounded.
 //
 // The rows of one KV head.  All G = q_heads / kv_heads query heads of a KV
 // head read the same keys, so a tile's rows are (token, head of the group)
@@ -45,12 +46,18 @@
 //
 // Masked places.  Scores of unseen keys are replaced, never added to;
 // values of slots past the sequence's end or on pages outside the cache are
-// replaced by zeros as they are expanded.  A NaN among the values of a key
-// that some rows of a tile see and others do not would reach the others as
-// 0 * NaN: in tiles that not every row sees whole, NaNs become zeros as they
-// are expanded, and where there was one (rare) the rows that see it get
-// their NaNs from the codes themselves (attn_poison).
+// replaced by zeros as they are expanded.  A NaN or infinity (a code under a
+// scale that takes it past BF16's range) among the values of a key that some
+// rows of a tile see and others do not would reach the others as 0 * NaN or
+// 0 * inf: in tiles that not every row sees whole they become zeros as they
+// are expanded.  Where there was one, or a sum is not finite at the end
+// (rare), the item's keys are looked through once more and the rows that see
+// one get it from the codes themselves (attn_special): a sum that sees an
+// infinity is that infinity whatever its weight, one that sees a NaN or both
+// infinities is NaN.
 #pragma once
+
+#include <type_traits>
 
 #include "mx_cache.hpp"
 #include "mx_splitk.hpp"
@@ -104,6 +111,16 @@ struct AttnItem {
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A wave-uniform v that the compiler knows nothing about: in a loop, addresses
+// made from it are computed where they are used, and not kept in registers
+// that are stepped beside it (mx_attn_tile: 18 registers in scratch memory and
+// 4096 tokens behind 12204 keys in 926 us, otherwise 825).
+__device__ __forceinline__ int opaque(int v)
+{
+    asm("" : "+s"(v));
+    return v;
+}
 
 // Inclusive sums over the wave's lanes (DPP row shifts and broadcasts).
 template <class T, int CTRL, int ROWS>
@@ -309,6 +326,10 @@ struct AttnGeom {
     static constexpr int CH = RB / 16;                      // chunks of a key
     static constexpr int VC = F == FMT_FP4 ? 32 : 16;       // values of a chunk
     static constexpr int NP = VC / 8;                       // pieces of eight
+    // a key's scales as they are loaded: the type of what a loop carries to its
+    // next turn (widened there; where the loop carries them widened, its end
+    // waits for the loads that it has just issued, 3% of a long E2M1 context)
+    typedef typename std::conditional<SB == 4, uint32_t, uint16_t>::type Scales;
 };
 
 // Page of key `key` of a sequence (its table row), or -1 past key1 or where
@@ -356,63 +377,100 @@ __device__ __forceinline__ void attn_expand(const u4v &c, unsigned s, u4v (&w)[N
     }
 }
 
-__device__ __forceinline__ bool bf16_nan(unsigned x) { return (x & 0x7FFFu) > 0x7F80u; }
+// NaN or infinity
+__device__ __forceinline__ bool bf16_special(unsigned x) { return (x & 0x7FFFu) >= 0x7F80u; }
 
 // A chunk of values of a tile that not every row sees whole: zeros for a key
-// that is not there and in the place of NaNs.  Returns whether there was one.
+// that is not there and in the place of NaNs and infinities.  Returns whether
+// there was one.
 template <int NP>
 __device__ __forceinline__ bool attn_clean(u4v (&w)[NP], bool ok)
 {
-    bool nan = false;
+    bool special = false;
 #pragma unroll
     for (int e = 0; e < NP; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const bool a = bf16_nan(w[e][i]), b = bf16_nan(w[e][i] >> 16);
-            nan |= a | b;
+            const bool a = bf16_special(w[e][i]), b = bf16_special(w[e][i] >> 16);
+            special |= a | b;
             w[e][i] = ok ? w[e][i] & ((a ? 0u : 0xFFFFu) | (b ? 0u : 0xFFFF0000u)) : 0u;
         }
-    return nan && ok;
+    return special && ok;
 }
 
-// Four consecutive values d .. d + 3 of a row of the cache: bit i set where
-// value d + i is a NaN.
+// Whether the values of a row of the cache may hold a NaN or an infinity: an
+// E4M3 NaN code, or a scale under which the largest code (448 or 6, with BF16's
+// 2^128 out of reach up to scale codes 246 and 252) is infinite, 255 included.
 template <int F, int D>
-__device__ __forceinline__ unsigned attn_nan4(const AttnArgs &p, long long at, int d)
+__device__ __forceinline__ bool attn_may_be_special(const AttnArgs &p, long long at)
 {
     using G = AttnGeom<F, D>;
-    unsigned m = p.scales[1][at * G::SB + d / 32] == 255u ? 15u : 0u;
-    if constexpr (F == FMT_FP8) {
-        const unsigned c = *reinterpret_cast<const unsigned *>(p.codes[1] + at * G::RB + d);
+    bool any = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            m |= (unsigned)((c >> (8 * i) & 0x7Fu) == 0x7Fu) << i;
-    }
-    return m;
+    for (int b = 0; b < G::SB; ++b)
+        any |= p.scales[1][at * G::SB + b] > (F == FMT_FP4 ? 252 : 246);
+    if constexpr (F == FMT_FP8)
+#pragma unroll
+        for (int c = 0; c < G::CH; ++c) {
+            const u4v w = *reinterpret_cast<const u4v *>(p.codes[1] + at * G::RB + 16 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                any |= (((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+        }
+    return any;
 }
 
-// The sums of this lane's row that see a NaN among the values of keys
-// [key, key + n) of a tile whose NaNs became zeros: bit 4 j + i for value
-// column(j) + i.  (As bits that are looked at after the last tile: written
-// into the sums here, in a branch, they would be copied in every tile.)
-template <int F, int D, int NG, class Column>
-__device__ __forceinline__ unsigned long long attn_poison(const AttnArgs &p, const int *table, const AttnItem &it, int key,
-                                                          int n, const AttnRow &row, Column &&column)
+__device__ __forceinline__ bool attn_finite(const float (&f)[8])
 {
-    static_assert(NG <= 16, "bits");
-    unsigned long long bits = 0;
-    for (int k = key; k < min(key + n, it.key1); ++k) {
-        const int page = attn_page(p, table, k, it.key1);
-        if (page < 0)
-            continue;
-        const long long at = attn_row_at(p, page, it.head, k);
-        const bool see = k >= row.lo && k < row.hi;
-        for (int j = 0; j < NG; ++j) {
-            const unsigned m = see ? attn_nan4<F, D>(p, at, column(j)) : 0u;
-            bits |= (unsigned long long)m << (4 * j);
+    float probe = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        probe = fmaf(f[e], 0.0f, probe);
+    return probe == probe;
+}
+
+// Put the NaNs and infinities that a lane's row sees among values col .. col + 7
+// of the item's keys into its sums f of these columns.  The whole wave looks
+// through 64 keys at a time and takes those that may hold one in turn: once
+// per item, and only where a sum is not finite or a value was replaced.
+template <int F, int D>
+__device__ __forceinline__ void attn_special(const AttnArgs &p, const int *table, const AttnItem &it, const AttnRow &row, int col,
+                                             float (&f)[8])
+{
+    using G = AttnGeom<F, D>;
+    unsigned pos = 0, neg = 0, nan = 0;
+    for (int key = it.key0; key < it.key1; key += 64) {
+        const int mine = key + ((int)threadIdx.x & 63), page = attn_page(p, table, mine, it.key1);
+        bool may = false;
+        if (page >= 0)
+            may = attn_may_be_special<F, D>(p, attn_row_at(p, page, it.head, mine));
+        unsigned long long left = __ballot(may);
+        while (left) {
+            const int i = __ffsll(left) - 1, k = key + i;
+            left &= left - 1;
+            const long long at = attn_row_at(p, lane_value(page, i), it.head, k);
+            const bool see = k >= row.lo && k < row.hi;
+            u2v c;
+            if constexpr (F == FMT_FP4)
+                c = u2v{*reinterpret_cast<const unsigned *>(p.codes[1] + at * G::RB + col / 2), 0u};
+            else
+                c = *reinterpret_cast<const u2v *>(p.codes[1] + at * G::RB + col);
+            const u4v w = mx_decode8<F>(c, p.scales[1][at * G::SB + col / 32]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const unsigned x = w[e >> 1] >> (16 * (e & 1)) & 0xFFFFu, bit = see ? 1u << e : 0u;
+                pos |= x == 0x7F80u ? bit : 0u;
+                neg |= x == 0xFF80u ? bit : 0u;
+                nan |= (x & 0x7FFFu) > 0x7F80u ? bit : 0u;
+            }
         }
     }
-    return bits;
+    nan |= pos & neg;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        f[e] = pos >> e & 1 ? __builtin_inff() : neg >> e & 1 ? -__builtin_inff() : f[e];
+        f[e] = nan >> e & 1 ? __builtin_nanf("") : f[e];
+    }
 }
 
 __device__ __forceinline__ bf16x8v as_bf16x8(u4v v) { return __builtin_bit_cast(bf16x8v, v); }
@@ -473,12 +531,13 @@ struct AttnSums {
         m = -__builtin_inff();
         l = 0.0f;
     }
-    // (sums of keys that the row does not see: m = -inf, l = 0, f = 0)
+    // (sums of keys that the row does not see: m = -inf, l = 0, f = 0.  The
+    // weights stay above 0, where an infinite sum would become NaN)
     __device__ __forceinline__ void add(const float (&g)[8], float mq, float lq)
     {
         const float mn = fmaxf(m, mq);
-        const float wa = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-        const float wb = mq == mn ? 1.0f : __builtin_amdgcn_exp2f(mq - mn);
+        const float wa = m == mn ? 1.0f : fmaxf(__builtin_amdgcn_exp2f(m - mn), 0x1p-149f);
+        const float wb = mq == mn ? 1.0f : fmaxf(__builtin_amdgcn_exp2f(mq - mn), 0x1p-149f);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             f[e] = f[e] * wa + g[e] * wb;
@@ -704,6 +763,7 @@ void mx_attn_rows(AttnArgs p)
     constexpr int BYTES = (WBYTES > OBYTES ? WBYTES : OBYTES) * 4;
     __shared__ __attribute__((aligned(1024))) char lds[BYTES];
     __shared__ float ml[4][BM][2];
+    __shared__ unsigned cleaned[4];                     // a wave replaced a value by a zero
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g = lane >> 4;
 
     AttnItem it;
@@ -734,7 +794,7 @@ void mx_attn_rows(AttnArgs p)
     char *mem = lds + wave * WBYTES;
     v4f o[QT][DT];
     float m[QT], l[QT];
-    unsigned long long poison[QT] = {};
+    bool replaced = false;          // a value, by a zero
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         // (0 for rows that are not there, whose scores are 0)
@@ -749,7 +809,9 @@ void mx_attn_rows(AttnArgs p)
     // scale codes, its chunks of values (key mykey + j KPL) with theirs, and
     // the keys of it that are there (bits).
     u4v kc[2][2], vc[NL];
-    unsigned ks[2], vs[NL], there = 0;
+    typename G::Scales ks[2];
+    uint8_t vs[NL];
+    unsigned there = 0;
     const int mykey = lane / G::CH, chunk = lane % G::CH;
     auto load = [&](int k) {
         const int page = attn_page_of(p, entry, k + (lane & 31), it.key1);
@@ -777,10 +839,7 @@ void mx_attn_rows(AttnArgs p)
                 if constexpr (KQ == 32)
                     kc[kt][1] = *reinterpret_cast<const u4v *>(c + (off * G::RB + 64 + 16 * g));
             }
-            if constexpr (G::SB == 4)
-                ks[kt] = *reinterpret_cast<const unsigned *>(s + off * 4);
-            else
-                ks[kt] = *reinterpret_cast<const uint16_t *>(s + off * 2);
+            ks[kt] = *reinterpret_cast<const typename G::Scales *>(s + off * G::SB);
         }
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
@@ -814,13 +873,12 @@ void mx_attn_rows(AttnArgs p)
         // values into LDS
         const bool whole = there == 0xFFFFFFFFu && key >= it.all_lo && key + KT <= it.all_hi;
         const unsigned here = there;
-        bool nan = false;
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
             u4v w[NP];
             attn_expand<F>(vc[j], vs[j], w);
             if (__builtin_expect(!whole, 0))
-                nan |= attn_clean(w, here >> (mykey + j * KPL) & 1);
+                replaced |= attn_clean(w, here >> (mykey + j * KPL) & 1);
 #pragma unroll
             for (int e = 0; e < NP; ++e)
                 *reinterpret_cast<u4v *>(vput + j * KPL * VROW + 16 * e) = w[e];
@@ -902,22 +960,12 @@ void mx_attn_rows(AttnArgs p)
                 o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, pb[t], o[t][d], 0, 0, 0);
         }
         wave_fence();
-        if (__builtin_expect(!whole && __any(nan), 0)) {
-#pragma unroll
-            for (int t = 0; t < QT; ++t)
-                poison[t] |= attn_poison<F, D, DT>(p, table, it, key, KT, row[t], [&](int j) { return 16 * j + 4 * g; });
-        }
     }
-#pragma unroll
-    for (int t = 0; t < QT; ++t)
-        if (__builtin_expect(__any(poison[t] != 0), 0))
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[t][d][i] = poison[t] >> (4 * d + i) & 1 ? __builtin_nanf("") : o[t][d][i];
 
     // join the four waves, 16 rows at a time
+    replaced = __any(replaced);
+    if (lane == 0)
+        cleaned[wave] = replaced;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         l[t] += __shfl_xor(l[t], 16);
@@ -974,6 +1022,17 @@ void mx_attn_rows(AttnArgs p)
             }
         }
         __syncthreads();
+    }
+    const bool cleans = cleaned[0] | cleaned[1] | cleaned[2] | cleaned[3];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+        const int i = tid + 256 * u;
+        if (i - lane >= BM * RUNS)
+            continue;
+        const AttnRow at = attn_row(p, it, it.row0 + i / RUNS);
+        // (a row with a NaN among its scores has l = NaN and becomes NaN)
+        if (__builtin_expect(__any(at.token >= 0 && fl[u] == fl[u] && (cleans || !attn_finite(f[u]))), 0))
+            attn_special<F, D>(p, table, it, at, i % RUNS * 8, f[u]);
     }
     static_assert(BYTES >= 40 * 256, "scratch");
     attn_finish<D, BM, 256>(p, it, tid, reinterpret_cast<float *>(lds), [&](int u, AttnSums &out) {
@@ -1066,7 +1125,7 @@ void mx_attn_tile(AttnArgs p)
     constexpr bool EVERY = 2 * SIDE >= THR, STATIC = SIDE >= THR;
     __shared__ __attribute__((aligned(1024))) char lds[BYTES];
     __shared__ float ml[BM][2];
-    __shared__ unsigned nans[VBUFS][NW];                // a NaN became a zero in the tile (by wave)
+    __shared__ unsigned cleaned[NW];                    // a wave replaced a value by a zero
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 31, h = lane >> 5;
 
     AttnItem it;
@@ -1112,7 +1171,6 @@ void mx_attn_tile(AttnArgs p)
             o[d][i] = 0.0f;
     // (0 for rows that are not there, whose scores are 0)
     float m = row.token >= 0 ? -__builtin_inff() : 0.0f, l = 0.0f;
-    unsigned long long poison = 0;
     bf16x8v pb[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -1190,21 +1248,20 @@ void mx_attn_tile(AttnArgs p)
         gone = loaded == ~0ull || t >= T ? gone : t;
         if (__builtin_expect(!(gone != t && all_full.has(t)), 0)) {
             char *vbuf = lds + KBUFS * KBYTES + (unsigned)t % VBUFS * VBYTES;
-            bool nan = false;
+            bool replaced = false;
 #pragma unroll
             for (int i = 0; i < NI; ++i)
                 if (side_of(i)) {
                     u4v w[NP];
                     attn_expand<F>(codes[i], scale[i], w);
-                    nan |= attn_clean(w, loaded >> (key_of(i) + mykey) & 1) && loads;
+                    replaced |= attn_clean(w, loaded >> (key_of(i) + mykey) & 1) && loads;
                     if (loads)
 #pragma unroll
                         for (int e = 0; e < NP; ++e)
                             *reinterpret_cast<u4v *>(vbuf + put_value(i, e)) = w[e];
                 }
-            const unsigned some = __any(nan);
-            if (lane == 0)
-                nans[(unsigned)t % VBUFS][wave] = some;
+            if (__any(replaced) && lane == 0)
+                cleaned[wave] = 1;
         }
     };
     auto expand = [&](int t) {
@@ -1302,7 +1359,8 @@ void mx_attn_tile(AttnArgs p)
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    auto phase_m = [&](int t) {
+    // (always inlined: as a call its arrays would live in scratch memory)
+    auto phase_m = [&](int t) __attribute__((always_inline)) {
         if constexpr (NW != 8)
             fetch(IntC<0>{}, t);
         fetch(IntC<1>{}, t);
@@ -1310,21 +1368,12 @@ void mx_attn_tile(AttnArgs p)
         __builtin_amdgcn_s_setprio(1);
         // No branches, so that the sums stay in their registers: where a wave
         // saw nothing of tile t - 1 its p are zeros, and the values finite (a
-        // tile that not every row sees whole holds no NaN); t = 0 takes tile
-        // 0's values for those before it.  Past the last tile the first
-        // product is not used.
+        // tile that not every row sees whole holds no NaN and no infinity);
+        // t = 0 takes tile 0's values for those before it, whose NaNs and
+        // infinities every row sees, and gets from attn_special, where it
+        // holds any.  Past the last tile the first product is not used.
         batches(t);
         __builtin_amdgcn_s_setprio(0);
-        if (__builtin_expect(!(t - 1 > gone && all_full.has(t - 1)) && some.has(t - 1), 0)) {
-            unsigned any = 0;
-#pragma unroll
-            for (int w = 0; w < NW; ++w)
-                any |= nans[(unsigned)(t - 1) % VBUFS][w];
-            // (of a whole tile in front of one with keys missing: nothing yet)
-            if (uniform(any))
-                poison |= attn_poison<F, D, DT * 4>(p, table, it, it.key0 + (t - 1) * BN, BN, row,
-                                                    [&](int j) { return 32 * (j >> 2) + 8 * (j & 3) + 4 * h; });
-        }
     };
     auto softmax = [&](int t) {
         if (__builtin_expect(!(t > gone && full.has(t)), 0)) {
@@ -1394,8 +1443,8 @@ void mx_attn_tile(AttnArgs p)
             load(t + 2);
         }
     };
-    if (lane < VBUFS)
-        nans[lane][wave] = 0;
+    if (lane == 0)
+        cleaned[wave] = 0;
     if (T > 0) {
         load(0);
         expand(0);
@@ -1404,13 +1453,15 @@ void mx_attn_tile(AttnArgs p)
         if constexpr (NW == 8)
             fetch(IntC<0>{}, 0);
         if (NW == 8 && wave >= 4) {
-            for (int t = 0; t < T; ++t) {
+            for (int i = 0; i < T; ++i) {
+                const int t = opaque(i);
                 phase_m(t);
                 block_barrier();
                 phase_v(t);
             }
         } else {
-            for (int t = 0; t < T; ++t) {
+            for (int i = 0; i < T; ++i) {
+                const int t = opaque(i);
                 phase_m(t);
                 if (NW != 8)
                     block_barrier();
@@ -1421,11 +1472,6 @@ void mx_attn_tile(AttnArgs p)
         phase_m(T);
     }
     __syncthreads();
-    if (__builtin_expect(__any(poison != 0), 0))
-#pragma unroll
-        for (int e = 0; e < 16 * DT; ++e)
-            o[e >> 4][e & 15] = poison >> e & 1 ? __builtin_nanf("") : o[e >> 4][e & 15];
-
     l += __shfl_xor(l, 32);
     if (h == 0) {
         ml[32 * wave + r][0] = m;
@@ -1441,7 +1487,11 @@ void mx_attn_tile(AttnArgs p)
     constexpr int RUNS = D / 8;
     const int n = min(BM, it.ntok * p.group - it.row0) * RUNS;
     const __amdgpu_buffer_rsrc_t slot = attn_slot<D, BM>(p, it, it.part);
-    for (int i = tid; i < n; i += THR) {
+    bool cleans = false;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+        cleans |= cleaned[w] != 0;
+    for (int i = tid; i - lane < n; i += THR) {         // (whole waves)
         const int rr = i / RUNS;
         const float *src = reinterpret_cast<const float *>(lds) + rr * OROW + i % RUNS * 8;
         AttnSums s;
@@ -1450,6 +1500,11 @@ void mx_attn_tile(AttnArgs p)
             s.f[e] = src[e];
         s.m = ml[rr][0];
         s.l = ml[rr][1];
+        // (a row with a NaN among its scores has l = NaN and becomes NaN)
+        if (__builtin_expect(__any(i < n && s.l == s.l && (cleans || !attn_finite(s.f))), 0))
+            attn_special<F, D>(p, table, it, attn_row(p, it, it.row0 + rr), i % RUNS * 8, s.f);
+        if (i >= n)
+            continue;
         if (it.parts == 1)
             attn_write<D>(p, it, i, s);
         else

@@ -95,7 +95,9 @@ void mx_cache_write(CacheArgs p)
 
 // Eight values of a block with E8M0 code s, as BF16 pairs: element times
 // 2^(s - 127), rounded to nearest even where a BF16 cannot hold it (blocks
-// of subnormal BF16 values only); NaN for s = 255 and for E4M3 NaN codes.
+// of subnormal BF16 values; past its range, which takes scales that no block of
+// finite values is written with, infinity); NaN for s = 255 and for E4M3 NaN
+// codes.
 // The conversions take s as an exponent field, 0 included, and give NaN for
 // every code under the field 255 (checked on MI355X for all codes under all
 // scales).

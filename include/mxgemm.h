@@ -394,7 +394,10 @@ typedef struct {
 /*
  * Write tokens into the cache, quantized as mx_quantize_bf16 does, and read
  * slots back as BF16 (element times scale; exact, but for blocks of subnormal
- * BF16 values, which round to nearest even; NaN for scale code 0xFF).
+ * BF16 values, which round to nearest even, and for values past BF16's range,
+ * which are infinities: E4M3 codes under scale codes of 247 and more, E2M1
+ * codes under 253 and more, as no block of finite values is written; NaN for
+ * scale code 0xFF).
  *
  * k, v       BF16, token t at element t * k_stride / t * v_stride, its
  *            kv_heads * head_dim values contiguous (so parts of the rows of a
@@ -453,9 +456,13 @@ int mx_kv_cache_read(const mxg_kv_cache_t *cache, void *k, void *v, int64_t k_st
  * ends are clamped to [previous end, tokens], lens to [0, table_width *
  * page_size]; keys on a page outside [0, pages) are as if they were not
  * there.  A row that sees no key gives zeros and lse = -inf.  Rows of q past
- * the last end are not written.  NaN among a key's values reaches only the
- * rows that see the key.  head_dim is 64 or 128.  p = exp(x - reference) is
- * rounded to BF16 for its product with the values; all sums are FP32.
+ * the last end are not written.  Keys and values are what mx_kv_cache_read
+ * gives.  NaN and infinities among a key's values reach only the rows that see
+ * the key, an infinity as itself whatever the key's weight (NaN with the other
+ * infinity, with a NaN, or where the row's scores hold a NaN).  head_dim is 64
+ * or 128.  p = exp(x - reference) is rounded to BF16 for its product with the
+ * values; all sums are FP32 and divided by the sum of the p's at the end (p
+ * reaches 4096: values of 2^100 and more may take the sums past FP32's range).
  *
  * MXG_ERR_NULL, MXG_ERR_DTYPE (out_dtype), MXG_ERR_SHAPE (sizes; seqs or
  * q_heads above 65536; tokens * q_heads above 2^30; table_width * page_size
