@@ -21,6 +21,12 @@ library is missing, importing this package raises.
 
 ``scaled_mm`` is the convenience form that allocates C and returns it.
 
+``workspace="auto"`` keeps one workspace per stream, which grows with the
+largest call.  A call that torch captures into a graph gets one of its own
+from the graph's memory instead, which the graph clears before it (a fill of
+64 KiB; with an explicit workspace, cleared once, there is none).  A graph
+captured by other means than torch's takes an explicit workspace.
+
 Around the products (see the same header):
 
     mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, stream=None)
@@ -133,8 +139,10 @@ def _ptr(t) -> int:
     return t.data_ptr()
 
 
-# the current stream's handle without the Stream object around it (3 us a call)
+# the current stream's handle without the Stream object around it (3 us a
+# call), and whether it is being captured
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_is_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 def _stream(stream) -> int:
@@ -169,26 +177,55 @@ def _out_code(c, out_dtype):
 
 
 _WORKSPACES = {}
+_COUNTER_BYTES = 65536          # of a workspace, at its start: zero before every call
 
 
-def _workspace(ws, nbytes, stream_ptr):
-    """(pointer, bytes) of the split-K workspace argument (see the module doc)."""
-    if ws is None or nbytes == 0:
-        return 0, 0
-    if isinstance(ws, torch.Tensor):
-        if not ws.is_cuda or not ws.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        return ws.data_ptr(), ws.numel() * ws.element_size()
-    if ws != "auto":
-        raise ValueError("workspace must be a tensor, None or 'auto'")
-    key = (_current_device(), stream_ptr)
+def _on_stream(stream_ptr):
+    """The context in which tensors are made, filled and, later, given back to
+    the allocator on that stream."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream_ptr))
+
+
+def _auto_workspace(nbytes, stream_ptr):
+    """The stream's workspace, or one for this call alone where it is captured:
+    a graph may be replayed after any later call of the stream, and before any
+    graph that was captured earlier."""
+    device = _current_device()
+    if stream_ptr == _raw_stream(device):
+        captured = _is_capturing()
+    else:
+        with _on_stream(stream_ptr):
+            captured = _is_capturing()
+    if captured:
+        with _on_stream(stream_ptr):
+            held = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+            held[:_COUNTER_BYTES].zero_()
+        return held
+    key = (device, stream_ptr)
     held = _WORKSPACES.get(key)
     if held is None or held.numel() < nbytes:
-        # filled and, later, given back to the allocator on the stream that uses it
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream_ptr)):
+        with _on_stream(stream_ptr):
             held = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
         _WORKSPACES[key] = held
-    return held.data_ptr(), held.numel()
+    return held
+
+
+def _call(name, fn, args, workspace, nbytes, stream_ptr):
+    """fn(*args, workspace, its bytes, stream) with the workspace argument of
+    the call (see the module doc), nbytes being what the call splits with."""
+    if workspace is None or nbytes == 0:
+        st = fn(*args, 0, 0, stream_ptr)
+    elif isinstance(workspace, torch.Tensor):
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream_ptr)
+    elif workspace == "auto":
+        held = _auto_workspace(nbytes, stream_ptr)
+        st = fn(*args, held.data_ptr(), held.numel(), stream_ptr)
+    else:
+        raise ValueError("workspace must be a tensor, None or 'auto'")
+    if st:
+        raise MxGemmError(st, name)
 
 
 def mx_scaled_mm_workspace_bytes(is_fp4, M, N, K) -> int:
@@ -202,11 +239,8 @@ def mx_config_workspace_bytes(variant, splits, M, N) -> int:
 def _default(is_fp4, a, b, a_scale, b_scale, c, M, N, K, out_dtype, workspace, stream, fn, name):
     _check_tensors(is_fp4, a, b, a_scale, b_scale, c, M, N, K)
     st_ptr = _stream(stream)
-    wp, wb = _workspace(workspace, mx_scaled_mm_workspace_bytes(is_fp4, M, N, K), st_ptr)
-    st = fn(_ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale), _ptr(c), M, N, K, _out_code(c, out_dtype),
-            wp, wb, st_ptr)
-    if st:
-        raise MxGemmError(st, name)
+    _call(name, fn, (_ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale), _ptr(c), M, N, K, _out_code(c, out_dtype)),
+          workspace, mx_scaled_mm_workspace_bytes(is_fp4, M, N, K), st_ptr)
 
 
 def mx_scaled_mm_fp4(a, b, a_scale, b_scale, c, M, N, K, out_dtype=None, workspace="auto",
@@ -225,11 +259,10 @@ def mx_scaled_mm_config(is_fp4, a, b, a_scale, b_scale, c, M, N, K, variant, spl
                         workspace="auto", out_dtype=None, stream=None) -> None:
     _check_tensors(bool(is_fp4), a, b, a_scale, b_scale, c, M, N, K)
     st_ptr = _stream(stream)
-    wp, wb = _workspace(workspace, mx_config_workspace_bytes(variant, splits, M, N), st_ptr)
-    st = _lib.mx_scaled_mm_config(int(bool(is_fp4)), _ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale),
-                                  _ptr(c), M, N, K, _out_code(c, out_dtype), variant, splits, wp, wb, st_ptr)
-    if st:
-        raise MxGemmError(st, "mx_scaled_mm_config")
+    _call("mx_scaled_mm_config", _lib.mx_scaled_mm_config,
+          (int(bool(is_fp4)), _ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale), _ptr(c), M, N, K,
+           _out_code(c, out_dtype), variant, splits),
+          workspace, mx_config_workspace_bytes(variant, splits, M, N), st_ptr)
 
 
 def mx_default_config(is_fp4, M, N, K, with_workspace=True):
@@ -701,13 +734,10 @@ def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, c
         max_new = tokens
     st_ptr = _stream(stream)
     need = _lib.mx_paged_attention_workspace_bytes(cache._ref, seqs, tokens, heads, max_new) if workspace is not None else 0
-    wp, wb = _workspace(workspace, need, st_ptr)
-    st = _lib.mx_paged_attention(cache._ref, q.data_ptr(), qs, ends.data_ptr(), lens.data_ptr(), table.data_ptr(),
-                                 table.shape[1], seqs, tokens, heads, max_new,
-                                 dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
-                                 kind, 0 if lse is None else lse.data_ptr(), wp, wb, st_ptr)
-    if st:
-        raise MxGemmError(st, "mx_paged_attention")
+    _call("mx_paged_attention", _lib.mx_paged_attention,
+          (cache._ref, q.data_ptr(), qs, ends.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1], seqs,
+           tokens, heads, max_new, dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
+           kind, 0 if lse is None else lse.data_ptr()), workspace, need, st_ptr)
 
 
 def paged_attention(cache, q, ends, lens, table, out_dtype=torch.bfloat16, **kw) -> torch.Tensor:
