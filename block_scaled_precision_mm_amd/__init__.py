@@ -22,7 +22,7 @@ library is missing, importing this package raises.
 ``scaled_mm`` is the convenience form that allocates C and returns it.
 
 ``workspace="auto"`` keeps one workspace per stream, which grows with the
-largest call.  A call that torch captures into a graph gets one of its own
+largest call; host threads that call on one stream take turns at it.  A call that torch captures into a graph gets one of its own
 from the graph's memory instead, which the graph clears before it (a fill of
 64 KiB; with an explicit workspace, cleared once, there is none).  A graph
 captured by other means than torch's takes an explicit workspace.
@@ -42,6 +42,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 import torch  # load torch's HIP runtime first so the library binds to the same one
 
@@ -176,7 +177,7 @@ def _out_code(c, out_dtype):
     raise ValueError("out_dtype is required when c is a raw pointer")
 
 
-_WORKSPACES = {}
+_WORKSPACES, _WORKSPACE_LOCKS = {}, {}      # by (device, stream)
 _COUNTER_BYTES = 65536          # of a workspace, at its start: zero before every call
 
 
@@ -186,11 +187,11 @@ def _on_stream(stream_ptr):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream_ptr))
 
 
-def _auto_workspace(nbytes, stream_ptr):
+def _auto_workspace(key, nbytes):
     """The stream's workspace, or one for this call alone where it is captured:
     a graph may be replayed after any later call of the stream, and before any
     graph that was captured earlier."""
-    device = _current_device()
+    device, stream_ptr = key
     if stream_ptr == _raw_stream(device):
         captured = _is_capturing()
     else:
@@ -201,7 +202,6 @@ def _auto_workspace(nbytes, stream_ptr):
             held = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
             held[:_COUNTER_BYTES].zero_()
         return held
-    key = (device, stream_ptr)
     held = _WORKSPACES.get(key)
     if held is None or held.numel() < nbytes:
         with _on_stream(stream_ptr):
@@ -220,8 +220,13 @@ def _call(name, fn, args, workspace, nbytes, stream_ptr):
             raise ValueError("workspace must be a contiguous CUDA tensor")
         st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream_ptr)
     elif workspace == "auto":
-        held = _auto_workspace(nbytes, stream_ptr)
-        st = fn(*args, held.data_ptr(), held.numel(), stream_ptr)
+        # one thread at a time from the lookup to the last launch: a call's second
+        # kernel reads what its first left in the workspace
+        key = (_current_device(), stream_ptr)
+        lock = _WORKSPACE_LOCKS.get(key) or _WORKSPACE_LOCKS.setdefault(key, threading.RLock())
+        with lock:
+            held = _auto_workspace(key, nbytes)
+            st = fn(*args, held.data_ptr(), held.numel(), stream_ptr)
     else:
         raise ValueError("workspace must be a tensor, None or 'auto'")
     if st:

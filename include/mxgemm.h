@@ -449,9 +449,11 @@ int mx_kv_cache_read(const mxg_kv_cache_t *cache, void *k, void *v, int64_t k_st
  *             bytes, its first 64 KiB zero when it is allocated and left zero
  *             by every call (one workspace serves these calls and the split-K
  *             products of a stream; a captured graph keeps its address, and
- *             needs it as long as it may be replayed).  NULL or too small: no
- *             splitting, the same results but for FP32 rounding, slower for
- *             few long sequences.
+ *             needs it as long as it may be replayed).  A call may launch
+ *             kernels that read what others left in it: calls that share a
+ *             workspace are not issued by two host threads at once, on one
+ *             stream either.  NULL or too small: no splitting, the same
+ *             results but for FP32 rounding, slower for few long sequences.
  *
  * Any content of ends, lens, table and the cache gives in-bounds accesses:
  * ends are clamped to [previous end, tokens], lens to [0, table_width *

@@ -5,6 +5,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import threading
+import time
 
 import pytest
 import torch
@@ -114,3 +116,55 @@ def test_the_stream_of_the_call_counts_and_not_the_current_one(gpu):
     assert gpu.made[gpu.owner(a[0])][1:] == (9, True)
     assert gpu.made[gpu.owner(gpu.call(SMALL)[0])][1:] == (7, False)
     assert gpu.current == 7
+
+
+@pytest.mark.parametrize("entry", ["mx_scaled_mm_fp4", "mx_scaled_mm_config"])
+def test_calls_of_several_threads_do_not_share_one_at_a_time(gpu, monkeypatch, entry):
+    # a call may launch twice, its second kernel reading what the first left in the workspace: no other call
+    # of the stream's workspace may come between them, nor replace it before the launch
+    inside, most, lock = {}, {}, threading.Lock()
+
+    def launch(*args):
+        stream = args[-1]
+        with lock:
+            inside[stream] = inside.get(stream, 0) + 1
+            most[stream] = max(most.get(stream, 0), inside[stream])
+        held = [t for t in mx._WORKSPACES.values() if t.data_ptr() == args[-3]]
+        assert len(held) == 1, "not the workspace that the stream holds"
+        time.sleep(0.002)
+        with lock:
+            inside[stream] -= 1
+        return 0
+
+    variant = mx.mx_default_config(True, *SMALL)[0]
+    monkeypatch.setattr(mx._lib, entry, launch)
+    failed = []
+
+    def work(i):
+        try:
+            for n in range(8):
+                if entry == "mx_scaled_mm_fp4":
+                    mx.mx_scaled_mm_fp4(A, A, A, A, A, *(LARGE if (i + n) % 3 == 0 else SMALL), out_dtype=0, stream=7)
+                else:
+                    mx.mx_scaled_mm_config(True, A, A, A, A, A, *SMALL, variant, splits=2 + (i + n) % 3, out_dtype=0, stream=7)
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not failed and most == {7: 1}
+
+
+def test_a_refused_call_leaves_the_workspace_free(gpu, monkeypatch):
+    monkeypatch.setattr(mx._lib, "mx_scaled_mm_fp4", lambda *args: -2)
+    for _ in range(2):
+        with pytest.raises(mx.MxGemmError):
+            gpu.call(SMALL)
+    monkeypatch.setattr(mx._lib, "mx_scaled_mm_fp4", gpu.launch)
+    t = threading.Thread(target=gpu.call, args=(SMALL,), daemon=True)
+    t.start()
+    t.join(10)
+    assert not t.is_alive() and len(gpu.calls) == 1
