@@ -19,7 +19,8 @@ the output dtype.  A non-zero status raises MxGemmError (the caller's cue to
 fall back to another implementation).  There is no CPU fallback: if the
 library is missing, importing this package raises.
 
-``scaled_mm`` is the convenience form that allocates C and returns it.
+``scaled_mm`` is the convenience form that allocates C and returns it.  Given
+a stream, the convenience forms allocate on it, as under torch.cuda.stream.
 
 ``workspace="auto"`` keeps one workspace per stream, which grows with the
 largest call; host threads that call on one stream take turns at it.  A call that torch captures into a graph gets one of its own
@@ -40,6 +41,7 @@ Around the products (see the same header):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -185,6 +187,12 @@ def _on_stream(stream_ptr):
     """The context in which tensors are made, filled and, later, given back to
     the allocator on that stream."""
     return torch.cuda.stream(torch.cuda.ExternalStream(stream_ptr))
+
+
+def _made_on(stream):
+    """The context for a convenience form's outputs: memory of the stream that
+    writes them (memory of the current stream may still be in use there)."""
+    return contextlib.nullcontext() if stream is None else _on_stream(_stream(stream))
 
 
 def _auto_workspace(key, nbytes):
@@ -525,7 +533,8 @@ def scaled_mm(a, b, a_scale, b_scale, fmt=None, M=None, N=None, K=None,
     elif fmt not in ("fp4", "fp8"):
         raise ValueError("fmt must be 'fp4' or 'fp8'")
     dev = a.device if isinstance(a, torch.Tensor) else torch.device("cuda")
-    c = torch.empty((M, N), dtype=out_dtype, device=dev)
+    with _made_on(stream):
+        c = torch.empty((M, N), dtype=out_dtype, device=dev)
     fn = mx_scaled_mm_fp4 if fmt == "fp4" else mx_scaled_mm_fp8
     fn(a, b, a_scale, b_scale, c, M, N, K, workspace=workspace, stream=stream)
     return c
@@ -611,15 +620,16 @@ def rmsnorm(x, weight, residual=None, eps=1e-6, out="fp8", stream=None):
     K = x.shape[-1]
     rows = x.numel() // K if K else 0
     lead = x.shape[:-1]
-    h = torch.empty_like(x) if residual is not None else None
     ys = None
-    if out in ("fp8", "fp4"):
-        y = torch.empty(lead + (K if out == "fp8" else K // 2,), dtype=torch.uint8, device=x.device)
-        ys = torch.empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
-        kind = OUT_MXFP8 if out == "fp8" else OUT_MXFP4
-    else:
-        y = torch.empty(x.shape, dtype=out, device=x.device)
-        kind = _OUT_OF_DTYPE[out]
+    with _made_on(stream):
+        h = torch.empty_like(x) if residual is not None else None
+        if out in ("fp8", "fp4"):
+            y = torch.empty(lead + (K if out == "fp8" else K // 2,), dtype=torch.uint8, device=x.device)
+            ys = torch.empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
+            kind = OUT_MXFP8 if out == "fp8" else OUT_MXFP4
+        else:
+            y = torch.empty(x.shape, dtype=out, device=x.device)
+            kind = _OUT_OF_DTYPE[out]
     mx_rmsnorm(x, residual, weight, h, y, ys, rows, K, eps, out_kind=kind, stream=stream)
     return y, ys, x if residual is None else h
 
@@ -745,8 +755,10 @@ def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, c
            kind, 0 if lse is None else lse.data_ptr()), workspace, need, st_ptr)
 
 
-def paged_attention(cache, q, ends, lens, table, out_dtype=torch.bfloat16, **kw) -> torch.Tensor:
-    """mx_paged_attention into a new tensor, which it returns."""
-    out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
-    mx_paged_attention(cache, q, ends, lens, table, out, **kw)
+def paged_attention(cache, q, ends, lens, table, out_dtype=torch.bfloat16, stream=None, **kw) -> torch.Tensor:
+    """mx_paged_attention into a new tensor, which it returns.  Rows of q past
+    the last end are not written."""
+    with _made_on(stream):
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    mx_paged_attention(cache, q, ends, lens, table, out, stream=stream, **kw)
     return out
