@@ -17,7 +17,8 @@ functions carry the C ABI's names (see ``include/mxgemm.h``):
 [M, K/32] / [N, K/32] E8M0 bytes, ``c`` is a contiguous [M, N] tensor of
 the output dtype.  A non-zero status raises MxGemmError (the caller's cue to
 fall back to another implementation).  There is no CPU fallback: if the
-library is missing, importing this package raises.
+library is missing, importing this package raises.  Tensors lie on the current
+device, on which the call is launched; others are refused (ValueError).
 
 ``scaled_mm`` is the convenience form that allocates C and returns it.  Given
 a stream, the convenience forms allocate on it, as under torch.cuda.stream.
@@ -148,9 +149,18 @@ _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cud
 _is_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
-def _stream(stream) -> int:
+def _here() -> int:
+    """The current device, whose streams the calls run on: tensors have to lie
+    on it.  Without a GPU a number that is no tensor's (-1 is the CPU's)."""
+    try:
+        return _current_device()
+    except RuntimeError:
+        return -2
+
+
+def _stream(stream, device=None) -> int:
     if stream is None:
-        return _raw_stream(_current_device())
+        return _raw_stream(_current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -158,17 +168,17 @@ def _stream(stream) -> int:
 
 def _check_tensors(is_fp4, a, b, sa, sb, c, M, N, K):
     """Shape/contiguity checks on torch tensors (ints pass through as raw pointers)."""
-    eb = K // 2 if is_fp4 else K
+    eb, dev = K // 2 if is_fp4 else K, _here()
     for name, t, rows, cols in (("a", a, M, eb), ("b", b, N, eb), ("a_scale", sa, M, K // 32),
                                 ("b_scale", sb, N, K // 32)):
         if isinstance(t, torch.Tensor):
-            if not t.is_cuda or not t.is_contiguous() or t.element_size() != 1:
-                raise ValueError("%s must be a contiguous 1-byte CUDA tensor" % name)
+            if t.get_device() != dev or not t.is_contiguous() or t.element_size() != 1:
+                raise ValueError("%s must be a contiguous 1-byte CUDA tensor on the current device" % name)
             if t.numel() != rows * cols:
                 raise ValueError("%s has %d bytes, expected %d x %d" % (name, t.numel(), rows, cols))
     if isinstance(c, torch.Tensor):
-        if not c.is_cuda or not c.is_contiguous() or c.numel() != M * N:
-            raise ValueError("c must be a contiguous CUDA tensor with M*N elements")
+        if c.get_device() != dev or not c.is_contiguous() or c.numel() != M * N:
+            raise ValueError("c must be a contiguous CUDA tensor with M*N elements on the current device")
 
 
 def _out_code(c, out_dtype):
@@ -199,8 +209,8 @@ def _auto_workspace(key, nbytes):
     """The stream's workspace, or one for this call alone where it is captured:
     a graph may be replayed after any later call of the stream, and before any
     graph that was captured earlier."""
-    device, stream_ptr = key
-    if stream_ptr == _raw_stream(device):
+    stream_ptr = key[1]
+    if stream_ptr == _raw_stream(key[0]):
         captured = _is_capturing()
     else:
         with _on_stream(stream_ptr):
@@ -218,19 +228,19 @@ def _auto_workspace(key, nbytes):
     return held
 
 
-def _call(name, fn, args, workspace, nbytes, stream_ptr):
+def _call(name, fn, args, workspace, nbytes, dev, stream_ptr):
     """fn(*args, workspace, its bytes, stream) with the workspace argument of
     the call (see the module doc), nbytes being what the call splits with."""
     if workspace is None or nbytes == 0:
         st = fn(*args, 0, 0, stream_ptr)
     elif isinstance(workspace, torch.Tensor):
-        if not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor on the current device")
         st = fn(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(), stream_ptr)
     elif workspace == "auto":
         # one thread at a time from the lookup to the last launch: a call's second
         # kernel reads what its first left in the workspace
-        key = (_current_device(), stream_ptr)
+        key = (dev, stream_ptr)
         lock = _WORKSPACE_LOCKS.get(key) or _WORKSPACE_LOCKS.setdefault(key, threading.RLock())
         with lock:
             held = _auto_workspace(key, nbytes)
@@ -251,9 +261,9 @@ def mx_config_workspace_bytes(variant, splits, M, N) -> int:
 
 def _default(is_fp4, a, b, a_scale, b_scale, c, M, N, K, out_dtype, workspace, stream, fn, name):
     _check_tensors(is_fp4, a, b, a_scale, b_scale, c, M, N, K)
-    st_ptr = _stream(stream)
+    dev = _here()
     _call(name, fn, (_ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale), _ptr(c), M, N, K, _out_code(c, out_dtype)),
-          workspace, mx_scaled_mm_workspace_bytes(is_fp4, M, N, K), st_ptr)
+          workspace, mx_scaled_mm_workspace_bytes(is_fp4, M, N, K), dev, _stream(stream, dev))
 
 
 def mx_scaled_mm_fp4(a, b, a_scale, b_scale, c, M, N, K, out_dtype=None, workspace="auto",
@@ -271,11 +281,11 @@ def mx_scaled_mm_fp8(a, b, a_scale, b_scale, c, M, N, K, out_dtype=None, workspa
 def mx_scaled_mm_config(is_fp4, a, b, a_scale, b_scale, c, M, N, K, variant, splits=1,
                         workspace="auto", out_dtype=None, stream=None) -> None:
     _check_tensors(bool(is_fp4), a, b, a_scale, b_scale, c, M, N, K)
-    st_ptr = _stream(stream)
+    dev = _here()
     _call("mx_scaled_mm_config", _lib.mx_scaled_mm_config,
           (int(bool(is_fp4)), _ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale), _ptr(c), M, N, K,
            _out_code(c, out_dtype), variant, splits),
-          workspace, mx_config_workspace_bytes(variant, splits, M, N), st_ptr)
+          workspace, mx_config_workspace_bytes(variant, splits, M, N), dev, _stream(stream, dev))
 
 
 def mx_default_config(is_fp4, M, N, K, with_workspace=True):
@@ -334,13 +344,14 @@ def mx_quantize_bf16(x, codes, scales, rows: int, K: int, is_fp4: bool, stream=N
     (E2M1, two per byte, even k low nibble) or [rows][K] (E4M3); scales:
     uint8 [rows][K/32] E8M0.  Argument marshalling only.
     """
+    dev = _here()
     if isinstance(x, torch.Tensor):
-        if not x.is_cuda or not x.is_contiguous() or x.element_size() != 2 or x.numel() != rows * K:
-            raise ValueError("x must be a contiguous 2-byte CUDA tensor with rows*K elements")
+        if x.get_device() != dev or not x.is_contiguous() or x.element_size() != 2 or x.numel() != rows * K:
+            raise ValueError("x must be a contiguous 2-byte CUDA tensor with rows*K elements on the current device")
     for name, t, n in (("codes", codes, rows * (K // 2 if is_fp4 else K)), ("scales", scales, rows * (K // 32))):
         if isinstance(t, torch.Tensor):
-            if not t.is_cuda or not t.is_contiguous() or t.element_size() != 1 or t.numel() != n:
-                raise ValueError("%s must be a contiguous 1-byte CUDA tensor of %d elements" % (name, n))
+            if t.get_device() != dev or not t.is_contiguous() or t.element_size() != 1 or t.numel() != n:
+                raise ValueError("%s must be a contiguous 1-byte CUDA tensor of %d elements on the current device" % (name, n))
     rc = _lib.mx_quantize_bf16(_ptr(x), _ptr(codes), _ptr(scales), rows, K, 1 if is_fp4 else 0,
                                _stream(stream))
     if rc != 0:
@@ -348,18 +359,18 @@ def mx_quantize_bf16(x, codes, scales, rows: int, K: int, is_fp4: bool, stream=N
 
 
 def _check_grouped(is_fp4, a, b, sa, sb, c, offs, groups, M, N, K):
-    eb = K // 2 if is_fp4 else K
+    eb, dev = K // 2 if is_fp4 else K, _here()
     for name, t, n in (("a", a, M * eb), ("b", b, groups * N * eb), ("a_scale", sa, M * (K // 32)),
                        ("b_scale", sb, groups * N * (K // 32))):
         if isinstance(t, torch.Tensor):
-            if not t.is_cuda or not t.is_contiguous() or t.element_size() != 1 or t.numel() != n:
-                raise ValueError("%s must be a contiguous 1-byte CUDA tensor of %d bytes" % (name, n))
+            if t.get_device() != dev or not t.is_contiguous() or t.element_size() != 1 or t.numel() != n:
+                raise ValueError("%s must be a contiguous 1-byte CUDA tensor of %d bytes on the current device" % (name, n))
     if isinstance(c, torch.Tensor):
-        if not c.is_cuda or not c.is_contiguous() or c.numel() != M * N:
-            raise ValueError("c must be a contiguous CUDA tensor with M*N elements")
+        if c.get_device() != dev or not c.is_contiguous() or c.numel() != M * N:
+            raise ValueError("c must be a contiguous CUDA tensor with M*N elements on the current device")
     if isinstance(offs, torch.Tensor):
-        if not offs.is_cuda or offs.dtype != torch.int32 or not offs.is_contiguous() or offs.numel() != groups:
-            raise ValueError("offs must be a contiguous int32 CUDA tensor of `groups` elements")
+        if offs.get_device() != dev or offs.dtype != torch.int32 or not offs.is_contiguous() or offs.numel() != groups:
+            raise ValueError("offs must be a contiguous int32 CUDA tensor of `groups` elements on the current device")
 
 
 def mx_grouped_mm_fp4(a, b, a_scale, b_scale, c, offs, groups, M, N, K, out_dtype=None,
@@ -420,13 +431,16 @@ def mx_scaled_mm_fused(is_fp4, a, b, a_scale, b_scale, bias, act, c, c_scale, M,
     _check_tensors(bool(is_fp4), a, b, a_scale, b_scale, None, M, N, K)
     if out_kind is None:
         out_kind = _out_code(c, None)
+    dev = _here()
     if isinstance(bias, torch.Tensor):
-        if not bias.is_cuda or bias.dtype != torch.bfloat16 or not bias.is_contiguous() or bias.numel() != N:
-            raise ValueError("bias must be a contiguous bfloat16 CUDA tensor of N elements")
+        if bias.get_device() != dev or bias.dtype != torch.bfloat16 or not bias.is_contiguous() or bias.numel() != N:
+            raise ValueError("bias must be a contiguous bfloat16 CUDA tensor of N elements on the current device")
     if isinstance(c, torch.Tensor):
         n = M * N if out_kind in (OUT_BF16, OUT_F16, OUT_F32, OUT_MXFP8) else M * N // 2
-        if not c.is_cuda or not c.is_contiguous() or c.numel() != n:
-            raise ValueError("c must be a contiguous CUDA tensor of %d elements" % n)
+        if c.get_device() != dev or not c.is_contiguous() or c.numel() != n:
+            raise ValueError("c must be a contiguous CUDA tensor of %d elements on the current device" % n)
+    if isinstance(c_scale, torch.Tensor) and c_scale.get_device() != dev:
+        raise ValueError("c_scale must be a CUDA tensor on the current device")
     st = _lib.mx_scaled_mm_fused(int(bool(is_fp4)), _ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale),
                                  _ptr(bias), act, _ptr(c), _ptr(c_scale), M, N, K, out_kind, variant,
                                  _stream(stream))
@@ -463,10 +477,11 @@ def mx_dense_gemm(a, b, c, M, N, K, trans_a=0, trans_b=0, dtype=None, out_dtype=
         if not isinstance(a, torch.Tensor):
             raise ValueError("dtype is required when a is a raw pointer")
         dtype = {torch.bfloat16: 0, torch.float16: 1}[a.dtype]
+    dev = _here()
     for name, t, n in (("a", a, M * K), ("b", b, N * K), ("c", c, M * N)):
         if isinstance(t, torch.Tensor):
-            if not t.is_cuda or not t.is_contiguous() or t.numel() != n:
-                raise ValueError("%s must be a contiguous CUDA tensor of %d elements" % (name, n))
+            if t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
+                raise ValueError("%s must be a contiguous CUDA tensor of %d elements on the current device" % (name, n))
     st = _lib.mx_dense_gemm(dtype, trans_a, trans_b, _ptr(a), _ptr(b), _ptr(c), M, N, K,
                             _out_code(c, out_dtype), _stream(stream))
     if st:
@@ -567,14 +582,14 @@ def mx_noalloc_scratch_bytes() -> int:
 _BF16 = torch.bfloat16
 
 
-def _bf16_ptr(name, t, n):
+def _bf16_ptr(name, t, n, dev):
     """Address of a contiguous bfloat16 CUDA tensor of n elements, a raw pointer itself, 0 for None."""
     if t is None:
         return 0
     if t.__class__ is int:
         return t
-    if t.dtype is not _BF16 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
-        raise ValueError("%s must be a contiguous bfloat16 CUDA tensor of %d elements" % (name, n))
+    if t.dtype is not _BF16 or t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
+        raise ValueError("%s must be a contiguous bfloat16 CUDA tensor of %d elements on the current device" % (name, n))
     return t.data_ptr()
 
 
@@ -584,9 +599,9 @@ def mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, 
     y: the output in its own dtype (BF16 / FP16 / FP32), or 1-byte E4M3 codes
     [rows][K] or E2M1 pairs [rows][K/2] with y_scale uint8 [rows][K/32]; a
     1-byte y takes its format from its size unless out_kind is given."""
-    n = rows * K
-    px, pr, ph = _bf16_ptr("x", x, n), _bf16_ptr("residual", residual, n), _bf16_ptr("h", h, n)
-    pw = _bf16_ptr("weight", weight, K)
+    n, dev = rows * K, _here()
+    px, pr, ph = _bf16_ptr("x", x, n, dev), _bf16_ptr("residual", residual, n, dev), _bf16_ptr("h", h, n, dev)
+    pw = _bf16_ptr("weight", weight, K, dev)
     if y.__class__ is int:
         if out_kind is None:
             raise ValueError("out_kind is required when y is a raw pointer")
@@ -597,18 +612,18 @@ def mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, 
             out_kind = _OUT_OF_DTYPE.get(y.dtype)
             if out_kind is None:
                 out_kind = OUT_MXFP8 if y.numel() == n else OUT_MXFP4
-        if not y.is_cuda or not y.is_contiguous() or size != (2, 2, 4, 1, 1)[out_kind] or \
+        if y.get_device() != dev or not y.is_contiguous() or size != (2, 2, 4, 1, 1)[out_kind] or \
                 y.numel() != (n // 2 if out_kind == OUT_MXFP4 else n):
-            raise ValueError("y must be a contiguous CUDA tensor of rows*K values of its output kind")
+            raise ValueError("y must be a contiguous CUDA tensor of rows*K values of its output kind on the current device")
         py = y.data_ptr()
     if y_scale is None or y_scale.__class__ is int:
         ps = y_scale or 0
     else:
-        if not y_scale.is_cuda or not y_scale.is_contiguous() or y_scale.element_size() != 1 or \
+        if y_scale.get_device() != dev or not y_scale.is_contiguous() or y_scale.element_size() != 1 or \
                 y_scale.numel() != rows * (K // 32):
-            raise ValueError("y_scale must be a contiguous 1-byte CUDA tensor of rows*K/32 elements")
+            raise ValueError("y_scale must be a contiguous 1-byte CUDA tensor of rows*K/32 elements on the current device")
         ps = y_scale.data_ptr()
-    st = _lib.mx_rmsnorm(px, pr, pw, ph, py, ps, rows, K, eps, out_kind, _stream(stream))
+    st = _lib.mx_rmsnorm(px, pr, pw, ph, py, ps, rows, K, eps, out_kind, _stream(stream, dev))
     if st:
         raise MxGemmError(st, "mx_rmsnorm")
 
@@ -645,7 +660,7 @@ class KVCache:
     [..][head_dim/2] E2M1 pairs ('fp4'), scales [..][head_dim/32] E8M0 bytes."""
 
     __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "fmt", "pages", "page_size", "kv_heads", "head_dim",
-                 "_struct", "_ref")
+                 "device", "_struct", "_ref")
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, fmt="fp8"):
         if fmt not in ("fp4", "fp8"):
@@ -653,15 +668,15 @@ class KVCache:
         if k_codes.dim() != 4:
             raise ValueError("codes must be [pages][kv_heads][page_size][bytes of a row]")
         pages, heads, size, row = (int(n) for n in k_codes.shape)
-        dim = row * 2 if fmt == "fp4" else row
+        dim, dev = row * 2 if fmt == "fp4" else row, k_codes.get_device()
         for name, t, last in (("k_codes", k_codes, row), ("k_scales", k_scales, dim // 32),
                               ("v_codes", v_codes, row), ("v_scales", v_scales, dim // 32)):
-            if not t.is_cuda or not t.is_contiguous() or t.element_size() != 1 or \
+            if dev < 0 or t.get_device() != dev or not t.is_contiguous() or t.element_size() != 1 or \
                     tuple(t.shape) != (pages, heads, size, last):
-                raise ValueError("%s must be a contiguous 1-byte CUDA tensor [%d][%d][%d][%d]"
+                raise ValueError("%s must be a contiguous 1-byte CUDA tensor [%d][%d][%d][%d], all on one device"
                                  % (name, pages, heads, size, last))
         self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.fmt = k_codes, k_scales, v_codes, v_scales, fmt
-        self.pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, size, dim
+        self.pages, self.kv_heads, self.page_size, self.head_dim, self.device = pages, heads, size, dim, dev
         self._struct = _KVCacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                       v_scales.data_ptr(), pages, size, heads, dim, int(fmt == "fp4"))
         self._ref = ctypes.addressof(self._struct)
@@ -675,11 +690,19 @@ class KVCache:
         return cls(*t, fmt=fmt)
 
 
-def _token_rows(name, t, tokens, heads, dim):
+def _cache_device(cache) -> int:
+    """The current device, which has to be the cache's."""
+    dev = _here()
+    if cache.device != dev:
+        raise ValueError("the cache lies on cuda:%d and not on the current device" % cache.device)
+    return dev
+
+
+def _token_rows(name, t, tokens, heads, dim, dev):
     """Stride between the tokens of a bfloat16 [tokens][heads][dim] tensor
     whose tokens may be apart (a part of the rows of a joint product)."""
-    if t.dtype is not _BF16 or not t.is_cuda or t.shape != (tokens, heads, dim):
-        raise ValueError("%s must be a bfloat16 CUDA tensor [%d][%d][%d]" % (name, tokens, heads, dim))
+    if t.dtype is not _BF16 or t.get_device() != dev or t.shape != (tokens, heads, dim):
+        raise ValueError("%s must be a bfloat16 CUDA tensor [%d][%d][%d] on the current device" % (name, tokens, heads, dim))
     if tokens == 0:
         return heads * dim
     s0, s1, s2 = t.stride()
@@ -689,12 +712,13 @@ def _token_rows(name, t, tokens, heads, dim):
 
 
 def _cache_call(fn, name, cache, k, v, slots, stream):
-    if slots.dtype is not torch.int64 or not slots.is_cuda or slots.dim() != 1 or not slots.is_contiguous():
-        raise ValueError("slots must be a contiguous one-dimensional int64 CUDA tensor")
+    dev = _cache_device(cache)
+    if slots.dtype is not torch.int64 or slots.get_device() != dev or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous one-dimensional int64 CUDA tensor on the current device")
     n = slots.shape[0]
-    ks = _token_rows("k", k, n, cache.kv_heads, cache.head_dim)
-    vs = _token_rows("v", v, n, cache.kv_heads, cache.head_dim)
-    st = fn(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), n, _stream(stream))
+    ks = _token_rows("k", k, n, cache.kv_heads, cache.head_dim, dev)
+    vs = _token_rows("v", v, n, cache.kv_heads, cache.head_dim, dev)
+    st = fn(cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), n, _stream(stream, dev))
     if st:
         raise MxGemmError(st, name)
 
@@ -716,9 +740,9 @@ def mx_paged_attention_workspace_bytes(cache, seqs, tokens, q_heads, max_new) ->
     return int(_lib.mx_paged_attention_workspace_bytes(cache._ref, seqs, tokens, q_heads, max_new))
 
 
-def _int32(name, t, shape):
-    if t.dtype is not torch.int32 or not t.is_cuda or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 CUDA tensor of shape %s" % (name, tuple(shape)))
+def _int32(name, t, shape, dev):
+    if t.dtype is not torch.int32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 CUDA tensor of shape %s on the current device" % (name, tuple(shape)))
 
 
 def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, causal=True, window=0,
@@ -733,26 +757,26 @@ def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, c
     seqs = ends.shape[0]
     if dim != cache.head_dim:
         raise ValueError("q has head_dim %d, the cache %d" % (dim, cache.head_dim))
-    qs = _token_rows("q", q, tokens, heads, dim)
-    _int32("ends", ends, (seqs,))
-    _int32("lens", lens, (seqs,))
+    dev = _cache_device(cache)
+    qs = _token_rows("q", q, tokens, heads, dim, dev)
+    _int32("ends", ends, (seqs,), dev)
+    _int32("lens", lens, (seqs,), dev)
     if table.dim() != 2:
         raise ValueError("table must be [seqs][pages of a sequence]")
-    _int32("table", table, (seqs, table.shape[1]))
+    _int32("table", table, (seqs, table.shape[1]), dev)
     kind = _OUT_OF_DTYPE.get(out.dtype)
-    if kind is None or not out.is_cuda or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be a contiguous CUDA tensor of q's shape in BF16, FP16 or FP32")
-    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_cuda or lse.shape != (tokens, heads) or
+    if kind is None or out.get_device() != dev or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous CUDA tensor of q's shape in BF16, FP16 or FP32 on the current device")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (tokens, heads) or
                             not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 CUDA tensor [tokens][q_heads]")
+        raise ValueError("lse must be a contiguous float32 CUDA tensor [tokens][q_heads] on the current device")
     if max_new is None:
         max_new = tokens
-    st_ptr = _stream(stream)
     need = _lib.mx_paged_attention_workspace_bytes(cache._ref, seqs, tokens, heads, max_new) if workspace is not None else 0
     _call("mx_paged_attention", _lib.mx_paged_attention,
           (cache._ref, q.data_ptr(), qs, ends.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1], seqs,
            tokens, heads, max_new, dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
-           kind, 0 if lse is None else lse.data_ptr()), workspace, need, st_ptr)
+           kind, 0 if lse is None else lse.data_ptr()), workspace, need, dev, _stream(stream, dev))
 
 
 def paged_attention(cache, q, ends, lens, table, out_dtype=torch.bfloat16, stream=None, **kw) -> torch.Tensor:
