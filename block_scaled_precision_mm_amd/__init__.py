@@ -418,6 +418,7 @@ def mx_grouped_default_variant(groups, M, N) -> int:
 
 
 OUT_BF16, OUT_F16, OUT_F32, OUT_MXFP8, OUT_MXFP4 = 0, 1, 2, 3, 4
+_SIZE_OF_OUT = {OUT_BF16: 2, OUT_F16: 2, OUT_F32: 4, OUT_MXFP8: 1, OUT_MXFP4: 1}
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU_TANH = 0, 1, 2, 3
 
 
@@ -612,7 +613,7 @@ def mx_rmsnorm(x, residual, weight, h, y, y_scale, rows, K, eps, out_kind=None, 
             out_kind = _OUT_OF_DTYPE.get(y.dtype)
             if out_kind is None:
                 out_kind = OUT_MXFP8 if y.numel() == n else OUT_MXFP4
-        if y.get_device() != dev or not y.is_contiguous() or size != (2, 2, 4, 1, 1)[out_kind] or \
+        if y.get_device() != dev or not y.is_contiguous() or size != _SIZE_OF_OUT.get(out_kind, size) or \
                 y.numel() != (n // 2 if out_kind == OUT_MXFP4 else n):
             raise ValueError("y must be a contiguous CUDA tensor of rows*K values of its output kind on the current device")
         py = y.data_ptr()

@@ -108,3 +108,13 @@ def test_tensors_are_refused_where_there_is_no_gpu(monkeypatch):
     x = torch.zeros(4, 64, dtype=BF)
     with pytest.raises(ValueError):
         mx.mx_rmsnorm(x, None, None, None, x, None, 4, 64, 1e-6)
+
+
+@pytest.mark.parametrize("kind", [-1, 5, 7])
+def test_an_output_kind_that_is_none_is_the_librarys_to_refuse(monkeypatch, kind):
+    # a status, as with raw pointers, and no IndexError
+    monkeypatch.setattr(mx, "_current_device", lambda: 0)
+    monkeypatch.setattr(mx, "_raw_stream", lambda device: 0)
+    with pytest.raises(mx.MxGemmError) as e:
+        mx.mx_rmsnorm(gpu((4, 64), BF), None, None, None, gpu((4, 64), BF), None, 4, 64, 1e-6, out_kind=kind)
+    assert e.value.status == -5
