@@ -377,7 +377,8 @@ int mx_paged_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_str
         return MXG_ERR_NULL;
     if (q_stride % 8)
         return MXG_ERR_K_ALIGN;
-    if (!(scale > 0.0f) || !isfinite(scale) || (causal != 0 && causal != 1))
+    const float c = scale * 1.4426950408889634f;        // exponents of 2
+    if (!(scale > 0.0f) || !isfinite(c) || (causal != 0 && causal != 1))
         return MXG_ERR_CONFIG;
     if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)workspace) & 15)
         return MXG_ERR_PTR_ALIGN;
@@ -405,7 +406,7 @@ int mx_paged_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_str
     a.lse = lse;
     a.q_stride = q_stride;
     a.table_stride = table_width;
-    a.c = scale * 1.4426950408889634f;
+    a.c = c;
     a.seqs = (int)seqs;
     a.tokens = (int)tokens;
     a.heads = (int)cache->kv_heads;

@@ -440,7 +440,7 @@ int mx_kv_cache_read(const mxg_kv_cache_t *cache, void *k, void *v, int64_t k_st
  * tokens      rows of q (and of out); q_heads a multiple of kv_heads.
  * max_new     the most new tokens of a sequence: chooses kernels, for speed
  *             only (any value gives the same results but for rounding).
- * scale       > 0, finite (usually 1 / sqrt(head_dim)).
+ * scale       > 0, at most 2^127 (usually 1 / sqrt(head_dim)).
  * out         [tokens][q_heads][head_dim] of out_dtype (BF16, FP16, FP32),
  *             contiguous, 16-byte aligned.
  * lse         FP32 [tokens][q_heads], or NULL.
