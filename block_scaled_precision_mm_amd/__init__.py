@@ -727,7 +727,7 @@ def _cache_call(fn, name, cache, k, v, slots, stream):
 def mx_kv_cache_write(cache, k, v, slots, stream=None) -> None:
     """Quantize tokens into cache slots (C ABI mx_kv_cache_write): k and v
     bfloat16 [tokens][kv_heads][head_dim], tokens may be apart; slots int64
-    [tokens], -1 to skip one."""
+    [tokens], -1 to skip one, the others distinct."""
     _cache_call(_lib.mx_kv_cache_write, "mx_kv_cache_write", cache, k, v, slots, stream)
 
 

@@ -405,8 +405,9 @@ typedef struct {
  *            strides multiples of 8 and at least kv_heads * head_dim.
  * slots      DEVICE memory, int64 [tokens], 8-byte aligned: each token's
  *            slot.  A slot outside the cache (-1, for padding) is skipped by
- *            a write and reads zeros.  Two tokens written to one slot leave
- *            either's values, block by block.
+ *            a write and reads zeros.  The slots of a write that lie in the
+ *            cache are distinct: two tokens written to one leave codes and
+ *            scales of both there, in no order.
  * tokens     >= 0 (0: nothing is enqueued, k, v, slots may be NULL); tokens *
  *            kv_heads * head_dim at most 2^33.
  *
