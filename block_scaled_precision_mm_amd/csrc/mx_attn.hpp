@@ -727,7 +727,7 @@ void mx_attn_join(AttnArgs p)
 // next tile's codes are in flight while one is worked on.  64 sequences of 100
 // to 16000 keys, 8 KV heads of 128, E4M3: 436 MB in 93 us, 4.7 TB/s (a second
 // tile in flight 100 us: its registers cost a wave); three of 60000 to 131072
-// in E2M1: 349 MB in 69 us, 5.1 TB/s; one of 1025 keys 9.7 us: the launch, the
+// in E2M1: 349 MB in 69 us, 5.1 TB/s; one of 1025 keys 9.8 us: the launch, the
 // plan, a few dependent loads and the join.
 //
 // v_mfma_f32_16x16x32_bf16, lane (r = l & 15, g = l >> 4): operands row r,
@@ -1061,7 +1061,7 @@ __device__ __forceinline__ int value_swizzle(int key)
 //            into LDS and the loads of tile t + 2's
 //     V(t)   the softmax of tile t: VALU
 // Bound: MFMA, and beside it VALU issue: 4096 tokens of 32 heads of 128 over
-// 8 KV heads behind 12204 keys in E4M3 (0.96 TFLOP) take 830 to 870 us, 1.1
+// 8 KV heads behind 12204 keys in E4M3 (0.96 TFLOP) take 820 to 861 us, 1.1
 // PFLOP/s; their MFMAs alone 526 us, with the LDS reads 575, with the softmax 785.
 //
 // With NW = 8 the two waves of a SIMD are of different groups (waves 0-3 and

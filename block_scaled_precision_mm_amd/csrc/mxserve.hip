@@ -203,7 +203,8 @@ constexpr int kAttnThreads[4] = {256, 256, 256, 512};
 // CUs.  (mx_attn_rows: with few row tiles each has many parts, whose join
 // costs: one sequence of 100000 keys 47 us cut into 512 parts, 54 into 1024;
 // 32 sequences of 16 rows over 4096 keys 50 and 57.  With 512 row tiles they
-// balance ragged lengths: 64 sequences of 100 to 16000 keys 100 and 95 us.)
+// balance ragged lengths: 64 sequences of 100 to 16000 keys 100 and 95 us.
+// Nothing between 256 and 512 row tiles was measured: the step may lie lower.)
 int attn_target(int which, int64_t pairs)      // (sequence, head) pairs
 {
     switch (which) {
@@ -252,7 +253,8 @@ AttnFn attn_fn(int which, bool fp4, int64_t dim, int64_t page_size)
 // Most rows (new tokens x heads of a group) of a sequence for mx_attn_rows,
 // which takes 32 at a time and so reads and expands a key once for each 32,
 // but cuts its keys finer and joins the parts itself, without a second
-// kernel.  That pays while there are few row tiles (8 KV heads of 128, E4M3):
+// kernel.  By the number of row tiles it gains more than it loses (8 KV heads
+// of 128, E4M3):
 //     row tiles  sequences, rows, keys   us, in tiles of 128
 //          32    1 of 128 over 2048       16   27
 //         128    1 of 512 over 2048       22   33  (over 32768 keys 110 and 92)
@@ -261,7 +263,9 @@ AttnFn attn_fn(int which, bool fp4, int64_t dim, int64_t page_size)
 //         512    32 of 64 over 4096       66   94  (E2M1 54 and 86)
 //        1024    32 of 128 over 4096     120  112
 //        4096    128 of 128 over 1024    165  107
-// and for 64 rows, two row tiles, nearly always (2048: 93 and 88).
+// and for 64 rows with 2048 row tiles 93 and 88.  So the rule gives away 20% for
+// 512 rows over 32768 keys and 6% there; the keys' numbers are on the device,
+// and only their bound, table_width * page_size, is known here.
 int attn_few_rows(int64_t row_tiles)        // of 32 rows, all heads
 {
     return row_tiles <= 128 ? 512 : row_tiles <= 256 ? 256 : 64;
