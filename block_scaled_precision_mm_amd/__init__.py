@@ -38,7 +38,18 @@ Around the products (see the same header):
     mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, causal=True, window=0,
                        max_new=None, workspace="auto", stream=None)
 
-``rmsnorm`` and ``paged_attention`` are their convenience forms.
+Beside them, for drafted tokens and for experts:
+
+    mx_rope_cache_write(cache, q, k, v, positions, slots, rope, q_out=None, interleaved=False, stream=None)
+    mx_tree_attention(cache, q, ends, lens, table, mask, out, lse=None, scale=None, window=0, max_new=None,
+                      workspace="auto", stream=None)
+    mx_moe_dispatch(x, experts, y, y_scale, offs, pos, workspace="auto", stream=None)
+    mx_moe_combine(y, pos, weights, out, stream=None)
+    mx_moe_combine_grad(d_out, y, pos, weights, d_y, d_y_scale=None, d_weights=None, stream=None)
+
+``rmsnorm``, ``paged_attention``, ``tree_attention``, ``moe_dispatch``,
+``moe_combine`` and ``moe_combine_grad`` are their convenience forms;
+``rope_table`` and ``tree_mask`` make the tables that the calls take.
 """
 from __future__ import annotations
 
@@ -104,7 +115,19 @@ _lib.mx_paged_attention.argtypes = [_P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, 
                                     _INT, _I64, _P, _INT, _P, _P, _SZ, _P]
 _lib.mx_paged_attention_workspace_bytes.argtypes = [_P, _I64, _I64, _I64, _I64]
 _lib.mx_paged_attention_workspace_bytes.restype = _SZ
-for _f in ("mx_rmsnorm", "mx_kv_cache_write", "mx_kv_cache_read", "mx_paged_attention", "mx_scaled_mm_fp4", "mx_scaled_mm_fp8", "mx_scaled_mm_config", "mx_num_variants",
+_lib.mx_rope_cache_write.argtypes = [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _INT,
+                                     _I64, _P]
+_lib.mx_tree_attention.argtypes = [_P, _P, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, ctypes.c_float,
+                                   _I64, _P, _INT, _P, _P, _SZ, _P]
+_lib.mx_tree_attention_workspace_bytes.argtypes = [_P, _I64, _I64, _I64, _I64]
+_lib.mx_tree_attention_workspace_bytes.restype = _SZ
+_lib.mx_moe_dispatch.argtypes = [_P, _P, _I64, _I64, _I64, _I64, _P, _P, _INT, _P, _P, _P, _SZ, _P]
+_lib.mx_moe_dispatch_workspace_bytes.argtypes = [_I64, _I64, _I64]
+_lib.mx_moe_dispatch_workspace_bytes.restype = _SZ
+_lib.mx_moe_combine.argtypes = [_P, _INT, _P, _P, _I64, _I64, _I64, _I64, _P, _INT, _P]
+_lib.mx_moe_combine_grad.argtypes = [_P, _P, _INT, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _INT, _P, _P]
+for _f in ("mx_rmsnorm", "mx_kv_cache_write", "mx_kv_cache_read", "mx_paged_attention", "mx_rope_cache_write",
+           "mx_tree_attention", "mx_moe_dispatch", "mx_moe_combine", "mx_moe_combine_grad", "mx_scaled_mm_fp4", "mx_scaled_mm_fp8", "mx_scaled_mm_config", "mx_num_variants",
            "mx_default_config", "mx_scaled_mm_noalloc",
            "mx_last_hip_error", "mx_abi_version", "mx_default_variant", "mx_quantize_bf16",
            "mx_grouped_mm_fp4", "mx_grouped_mm_fp8", "mx_grouped_mm_config",
@@ -123,7 +146,9 @@ EXPORTS = ("mx_scaled_mm_fp4", "mx_scaled_mm_fp8", "mx_scaled_mm_config", "mx_nu
            "mx_scaled_mm_fused", "mx_fused_num_variants", "mx_fused_variant_name",
            "mx_fused_default_variant", "mx_fused_variant_max_k", "mx_dense_gemm", "mx_empty_like",
            "mx_rmsnorm", "mx_kv_cache_write", "mx_kv_cache_read", "mx_paged_attention",
-           "mx_paged_attention_workspace_bytes")
+           "mx_paged_attention_workspace_bytes", "mx_rope_cache_write", "mx_tree_attention",
+           "mx_tree_attention_workspace_bytes", "mx_moe_dispatch", "mx_moe_dispatch_workspace_bytes",
+           "mx_moe_combine", "mx_moe_combine_grad")
 
 
 class MxGemmError(RuntimeError):
@@ -746,14 +771,9 @@ def _int32(name, t, shape, dev):
         raise ValueError("%s must be a contiguous int32 CUDA tensor of shape %s on the current device" % (name, tuple(shape)))
 
 
-def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, causal=True, window=0,
-                       max_new=None, workspace="auto", stream=None) -> None:
-    """Attention of new tokens over the paged cache (C ABI
-    mx_paged_attention): q bfloat16 [tokens][q_heads][head_dim], tokens may be
-    apart; ends and lens int32 [seqs]; table int32 [seqs][pages of a
-    sequence]; out contiguous [tokens][q_heads][head_dim] in BF16 / FP16 /
-    FP32; lse float32 [tokens][q_heads] or None.  scale: 1/sqrt(head_dim) if
-    None; max_new: the most new tokens of a sequence, if known (for speed)."""
+def _attention(name, fn, need_fn, cache, q, ends, lens, table, out, lse, scale, window, max_new, workspace, stream, mask,
+               causal):
+    """mx_paged_attention, or with a mask mx_tree_attention."""
     tokens, heads, dim = q.shape
     seqs = ends.shape[0]
     if dim != cache.head_dim:
@@ -773,11 +793,30 @@ def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, c
         raise ValueError("lse must be a contiguous float32 CUDA tensor [tokens][q_heads] on the current device")
     if max_new is None:
         max_new = tokens
-    need = _lib.mx_paged_attention_workspace_bytes(cache._ref, seqs, tokens, heads, max_new) if workspace is not None else 0
-    _call("mx_paged_attention", _lib.mx_paged_attention,
-          (cache._ref, q.data_ptr(), qs, ends.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1], seqs,
-           tokens, heads, max_new, dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
-           kind, 0 if lse is None else lse.data_ptr()), workspace, need, dev, _stream(stream, dev))
+    scale = dim ** -0.5 if scale is None else scale
+    need = need_fn(cache._ref, seqs, tokens, heads, max_new) if workspace is not None else 0
+    head = (cache._ref, q.data_ptr(), qs, ends.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1])
+    if mask is None:
+        middle = (seqs, tokens, heads, max_new, scale, int(causal), window)
+    else:
+        if mask.dtype is not torch.int64 or mask.get_device() != dev or mask.dim() != 2 or mask.shape[0] != tokens or \
+                not mask.is_contiguous():
+            raise ValueError("mask must be a contiguous int64 CUDA tensor [tokens][words] on the current device")
+        middle = (mask.data_ptr(), mask.shape[1], seqs, tokens, heads, max_new, scale, window)
+    _call(name, fn, head + middle + (out.data_ptr(), kind, 0 if lse is None else lse.data_ptr()), workspace, need, dev,
+          _stream(stream, dev))
+
+
+def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, causal=True, window=0,
+                       max_new=None, workspace="auto", stream=None) -> None:
+    """Attention of new tokens over the paged cache (C ABI
+    mx_paged_attention): q bfloat16 [tokens][q_heads][head_dim], tokens may be
+    apart; ends and lens int32 [seqs]; table int32 [seqs][pages of a
+    sequence]; out contiguous [tokens][q_heads][head_dim] in BF16 / FP16 /
+    FP32; lse float32 [tokens][q_heads] or None.  scale: 1/sqrt(head_dim) if
+    None; max_new: the most new tokens of a sequence, if known (for speed)."""
+    _attention("mx_paged_attention", _lib.mx_paged_attention, _lib.mx_paged_attention_workspace_bytes, cache, q, ends,
+               lens, table, out, lse, scale, window, max_new, workspace, stream, None, causal)
 
 
 def paged_attention(cache, q, ends, lens, table, out_dtype=torch.bfloat16, stream=None, **kw) -> torch.Tensor:
@@ -787,3 +826,246 @@ def paged_attention(cache, q, ends, lens, table, out_dtype=torch.bfloat16, strea
         out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     mx_paged_attention(cache, q, ends, lens, table, out, stream=stream, **kw)
     return out
+
+
+def mx_tree_attention_workspace_bytes(cache, seqs, tokens, q_heads, max_new) -> int:
+    return int(_lib.mx_tree_attention_workspace_bytes(cache._ref, seqs, tokens, q_heads, max_new))
+
+
+def mx_tree_attention(cache, q, ends, lens, table, mask, out, lse=None, scale=None, window=0, max_new=None,
+                      workspace="auto", stream=None) -> None:
+    """Attention of trees of drafted tokens over the paged cache (C ABI
+    mx_tree_attention): mask int64 [tokens][words], bit j % 64 of word j / 64
+    of a token's row set where it sees the j-th new token of its sequence,
+    itself included (tree_mask makes it from parents); all else as for
+    mx_paged_attention."""
+    if mask is None:
+        raise ValueError("mask must be a contiguous int64 CUDA tensor [tokens][words] on the current device")
+    _attention("mx_tree_attention", _lib.mx_tree_attention, _lib.mx_tree_attention_workspace_bytes, cache, q, ends, lens,
+               table, out, lse, scale, window, max_new, workspace, stream, mask, False)
+
+
+def tree_attention(cache, q, ends, lens, table, mask, out_dtype=torch.bfloat16, stream=None, **kw) -> torch.Tensor:
+    """mx_tree_attention into a new tensor, which it returns.  Rows of q past
+    the last end are not written."""
+    with _made_on(stream):
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    mx_tree_attention(cache, q, ends, lens, table, mask, out, stream=stream, **kw)
+    return out
+
+
+def tree_mask(parents, words=None) -> torch.Tensor:
+    """The mask rows of one sequence's tree: parents a list, for each node the
+    earlier node that it continues, or -1 for one that continues the context.
+    int64 [nodes][words] on the CPU."""
+    rows = []
+    for i, parent in enumerate(parents):
+        if not -1 <= parent < i:
+            raise ValueError("node %d: its parent %d is not an earlier node or -1" % (i, parent))
+        rows.append((rows[parent] if parent >= 0 else 0) | 1 << i)
+    need = max(1, -(-len(rows) // 64))
+    words = need if words is None else words
+    if words < need:
+        raise ValueError("%d nodes need %d words" % (len(rows), need))
+    signed = lambda w: w - (1 << 64) if w >> 63 else w  # noqa: E731
+    return torch.tensor([[signed(r >> 64 * w & (1 << 64) - 1) for w in range(words)] for r in rows],
+                        dtype=torch.int64).view(len(rows), words)
+
+
+def rope_table(positions, rot, base=10000.0, device="cuda") -> torch.Tensor:
+    """float32 [positions][rot / 2][2]: cosine and sine of p * base^(-2 i / rot)
+    for mx_rope_cache_write, from angles in 64 bits."""
+    p = torch.arange(positions, dtype=torch.float64, device=device)
+    angle = p[:, None] * float(base) ** (torch.arange(0, rot, 2, dtype=torch.float64, device=device) / -rot)
+    return torch.stack((angle.cos(), angle.sin()), -1).float()
+
+
+def _int64(name, t, shape, dev):
+    if t.dtype is not torch.int64 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int64 CUDA tensor of shape %s on the current device" % (name, tuple(shape)))
+
+
+def mx_rope_cache_write(cache, q, k, v, positions, slots, rope, q_out=None, interleaved=False, stream=None) -> None:
+    """Rotate queries and keys by their positions and quantize keys and values
+    into cache slots (C ABI mx_rope_cache_write): q bfloat16
+    [tokens][q_heads][head_dim] (or None: keys and values only) into q_out, q
+    itself if None; k and v [tokens][kv_heads][head_dim]; the tokens of each may
+    be apart; positions and slots int64 [tokens]; rope float32
+    [positions][rot / 2][2] (rope_table)."""
+    dev = _cache_device(cache)
+    if slots.dim() != 1:
+        raise ValueError("slots must be a contiguous one-dimensional int64 CUDA tensor on the current device")
+    n, dim = slots.shape[0], cache.head_dim
+    _int64("slots", slots, (n,), dev)
+    _int64("positions", positions, (n,), dev)
+    ks = _token_rows("k", k, n, cache.kv_heads, dim, dev)
+    vs = _token_rows("v", v, n, cache.kv_heads, dim, dev)
+    if rope.dtype is not torch.float32 or rope.get_device() != dev or rope.dim() != 3 or rope.shape[2] != 2 or \
+            not rope.is_contiguous():
+        raise ValueError("rope must be a contiguous float32 CUDA tensor [positions][rot / 2][2] on the current device")
+    heads = qs = os_ = pq = po = 0
+    if q is not None:
+        if q_out is None:
+            q_out = q
+        heads = q.shape[1] if q.dim() == 3 else 0
+        qs, os_ = _token_rows("q", q, n, heads, dim, dev), _token_rows("q_out", q_out, n, heads, dim, dev)
+        pq, po = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    st = _lib.mx_rope_cache_write(cache._ref, pq, po, k.data_ptr(), v.data_ptr(), heads, qs, os_, ks, vs,
+                                  positions.data_ptr(), slots.data_ptr(), rope.data_ptr(), rope.shape[0], 2 * rope.shape[1],
+                                  int(interleaved), n, _stream(stream, dev))
+    if st:
+        raise MxGemmError(st, "mx_rope_cache_write")
+
+
+def mx_moe_dispatch_workspace_bytes(tokens, top_k, groups) -> int:
+    return int(_lib.mx_moe_dispatch_workspace_bytes(tokens, top_k, groups))
+
+
+def _rows(name, t, rows, width, dev, dtype=None):
+    """A contiguous [rows][width] CUDA tensor (of rows, if given)."""
+    if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows) or t.get_device() != dev or \
+            not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
+        raise ValueError("%s must be a contiguous %sCUDA tensor [%s][%d] on the current device"
+                         % (name, "" if dtype is None else "%s " % str(dtype).replace("torch.", ""),
+                            "rows" if rows is None else rows, width))
+
+
+def _mx_kind(name, y, y_scale, rows, width, dev):
+    """Output kind of y [rows][..] by its type and size: BF16 (y_scale ignored), or MX codes with y_scale."""
+    if y.dtype is _BF16:
+        _rows(name, y, rows, width, dev)
+        return OUT_BF16
+    if y.element_size() != 1 or y.dim() != 2:
+        raise ValueError("%s must be bfloat16, or 1-byte codes with scales" % name)
+    kind = OUT_MXFP8 if y.shape[1] == width else OUT_MXFP4
+    _rows(name, y, rows, width if kind == OUT_MXFP8 else width // 2, dev)
+    if y_scale is None or y_scale.element_size() != 1:
+        raise ValueError("%s_scale must be a contiguous 1-byte CUDA tensor [rows][%d] on the current device" % (name, width // 32))
+    _rows(name + "_scale", y_scale, rows, width // 32, dev)
+    return kind
+
+
+def mx_moe_dispatch(x, experts, y, y_scale, offs, pos, workspace="auto", stream=None) -> None:
+    """Tokens sorted by expert into the grouped product's A operand (C ABI
+    mx_moe_dispatch): x bfloat16 [tokens][K]; experts int64 [tokens][top_k],
+    ids outside [0, groups) without a row; y [tokens * top_k][..] bfloat16, or
+    1-byte E4M3 codes or E2M1 pairs with y_scale [tokens * top_k][K / 32];
+    offs int32 [groups] and pos int32 [tokens][top_k] are written."""
+    dev = _here()
+    tokens, K = x.shape
+    _rows("x", x, tokens, K, dev, _BF16)
+    if experts.dim() != 2 or offs.dim() != 1:
+        raise ValueError("experts must be [tokens][top_k] and offs [groups]")
+    top_k, groups = experts.shape[1], offs.shape[0]
+    _int64("experts", experts, (tokens, top_k), dev)
+    kind = _mx_kind("y", y, y_scale, tokens * top_k, K, dev)
+    _int32("offs", offs, (groups,), dev)
+    _int32("pos", pos, (tokens, top_k), dev)
+    need = _lib.mx_moe_dispatch_workspace_bytes(tokens, top_k, groups)
+    _call("mx_moe_dispatch", _lib.mx_moe_dispatch,
+          (x.data_ptr(), experts.data_ptr(), tokens, top_k, groups, K, y.data_ptr(), 0 if kind == OUT_BF16 else y_scale.data_ptr(),
+           kind, offs.data_ptr(), pos.data_ptr()), workspace, need, dev, _stream(stream, dev))
+
+
+def moe_dispatch(x, experts, groups, out="fp8", workspace="auto", stream=None):
+    """(y, y_scale, offs, pos) of mx_moe_dispatch in new tensors: out 'fp8',
+    'fp4' (codes and E8M0 scales, uint8) or torch.bfloat16 (y_scale None)."""
+    tokens, K = x.shape
+    rows = tokens * experts.shape[1]
+    ys = None
+    with _made_on(stream):
+        if out in ("fp8", "fp4"):
+            y = torch.empty((rows, K if out == "fp8" else K // 2), dtype=torch.uint8, device=x.device)
+            ys = torch.empty((rows, K // 32), dtype=torch.uint8, device=x.device)
+        elif out is _BF16:
+            y = torch.empty((rows, K), dtype=out, device=x.device)
+        else:
+            raise ValueError("out must be 'fp8', 'fp4' or torch.bfloat16")
+        offs = torch.empty((groups,), dtype=torch.int32, device=x.device)
+        pos = torch.empty((tokens, experts.shape[1]), dtype=torch.int32, device=x.device)
+    mx_moe_dispatch(x, experts, y, ys, offs, pos, workspace=workspace, stream=stream)
+    return y, ys, offs, pos
+
+
+def _combine_args(pos, weights, dev):
+    if pos.dim() != 2:
+        raise ValueError("pos must be [tokens][top_k]")
+    tokens, top_k = pos.shape
+    _int32("pos", pos, (tokens, top_k), dev)
+    if weights is not None:
+        _rows("weights", weights, tokens, top_k, dev, torch.float32)
+    return tokens, top_k, 0 if weights is None else weights.data_ptr()
+
+
+def _float_kind(name, t):
+    kind = _OUT_OF_DTYPE.get(t.dtype)
+    if kind is None or t.dim() != 2:
+        raise ValueError("%s must be a two-dimensional tensor in BF16, FP16 or FP32" % name)
+    return kind
+
+
+def mx_moe_combine(y, pos, weights, out, stream=None) -> None:
+    """The experts' rows back to their tokens (C ABI mx_moe_combine): y
+    [rows][N], pos int32 [tokens][top_k], weights float32 [tokens][top_k] or
+    None for ones, out [tokens][N]; y and out each BF16, FP16 or FP32.  Without
+    weights it is the gradient of mx_moe_dispatch."""
+    dev = _here()
+    tokens, top_k, pw = _combine_args(pos, weights, dev)
+    ky, ko = _float_kind("y", y), _float_kind("out", out)
+    rows, N = y.shape
+    _rows("y", y, rows, N, dev)
+    _rows("out", out, tokens, N, dev)
+    st = _lib.mx_moe_combine(y.data_ptr(), ky, pos.data_ptr(), pw, tokens, top_k, rows, N, out.data_ptr(), ko,
+                             _stream(stream, dev))
+    if st:
+        raise MxGemmError(st, "mx_moe_combine")
+
+
+def moe_combine(y, pos, weights=None, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """mx_moe_combine into a new tensor, which it returns."""
+    with _made_on(stream):
+        out = torch.empty((pos.shape[0], y.shape[1]), dtype=out_dtype, device=y.device)
+    mx_moe_combine(y, pos, weights, out, stream=stream)
+    return out
+
+
+def mx_moe_combine_grad(d_out, y, pos, weights, d_y, d_y_scale=None, d_weights=None, stream=None) -> None:
+    """The gradients of mx_moe_combine (C ABI mx_moe_combine_grad): d_out
+    [tokens][N] and y [rows][N] of one type; d_y [rows][N] of that type, or
+    1-byte E4M3 codes or E2M1 pairs with d_y_scale [rows][N / 32]; d_weights
+    float32 [tokens][top_k] or None (then y may be None)."""
+    dev = _here()
+    tokens, top_k, pw = _combine_args(pos, weights, dev)
+    dtype = _float_kind("d_out", d_out)
+    N, rows = d_out.shape[1], d_y.shape[0]
+    _rows("d_out", d_out, tokens, N, dev)
+    if d_y.dtype is d_out.dtype:
+        _rows("d_y", d_y, rows, N, dev)
+        kind = dtype
+    elif d_y.element_size() == 1:
+        kind = _mx_kind("d_y", d_y, d_y_scale, rows, N, dev)
+    else:
+        raise ValueError("d_y must be of d_out's type, or 1-byte codes with scales")
+    if d_weights is not None:
+        _rows("d_weights", d_weights, tokens, top_k, dev, torch.float32)
+        if y is None:
+            raise ValueError("y is needed for d_weights")
+    if y is not None:
+        _rows("y", y, rows, N, dev, d_out.dtype)
+    st = _lib.mx_moe_combine_grad(d_out.data_ptr(), 0 if y is None else y.data_ptr(), dtype, pos.data_ptr(), pw, tokens, top_k,
+                                  rows, N, d_y.data_ptr(), 0 if kind == dtype else d_y_scale.data_ptr(), kind,
+                                  0 if d_weights is None else d_weights.data_ptr(), _stream(stream, dev))
+    if st:
+        raise MxGemmError(st, "mx_moe_combine_grad")
+
+
+def moe_combine_grad(d_out, y, pos, weights=None, stream=None):
+    """(d_y, d_weights) of mx_moe_combine_grad in new tensors; rows of d_y that
+    no token has are zeros."""
+    with _made_on(stream):
+        d_y = torch.zeros(y.shape, dtype=y.dtype, device=y.device)
+        d_w = torch.empty(pos.shape, dtype=torch.float32, device=y.device)
+    mx_moe_combine_grad(d_out, y, pos, weights, d_y, None, d_w, stream=stream)
+    return d_y, d_w

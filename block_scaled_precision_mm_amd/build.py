@@ -10,7 +10,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmxgemm.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("mxgemm.hip", "mxserve.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("mxgemm.hip", "mxserve.hip", "mxdraft.hip", "mxmoe.hip")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".hpp", ".h"))] + \
     [os.path.join(ROOT, "include", "mxgemm.h")]
 

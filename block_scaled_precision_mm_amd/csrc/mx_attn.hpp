@@ -98,6 +98,8 @@ struct AttnArgs {
     int out_kind;
     int rows_above, rows_upto;              // the sequences of this launch: rows_above < n * group <= rows_upto
     float per_target;                       // KV heads / workgroups that can run at once
+    const unsigned long long *mask;         // trees of drafted tokens: [tokens][mask_words], the nodes that each sees
+    int mask_words;
 };
 
 // One workgroup's work.
@@ -205,7 +207,7 @@ __device__ __forceinline__ int cdiv_u(int a, int b) { return (int)(((unsigned)a 
 // twice that number of parts in all, which bounds the workspace, and the
 // items are at most one per row tile and that number more, which bounds the
 // grid (the factor keeps both with the FP32 total's rounding).
-template <int BM, int BN, int JOIN = 0>
+template <int TREE, int BM, int BN, int JOIN = 0>
 __device__ __forceinline__ bool plan_item(const AttnArgs &p, int item, int min_tiles, AttnItem &it)
 {
     const int lane = threadIdx.x & 63;
@@ -271,11 +273,12 @@ __device__ __forceinline__ bool plan_item(const AttnArgs &p, int item, int min_t
         it.slot_step = rtiles * p.heads;
         // the keys that some row of the tile sees, and those that all do
         const int t0 = p.by_group.div(it.row0), t1 = min(p.by_group.div(it.row0 + BM - 1), it.ntok - 1);
-        const int pos0 = it.len - it.ntok + t0, pos1 = it.len - it.ntok + t1;
-        const int hi = p.causal ? min(max(pos1 + 1, 0), it.len) : it.len;
+        // (a tree's rows: the keys of the context, whatever their masks and depths)
+        const int pos0 = it.len - it.ntok + (TREE ? 0 : t0), pos1 = TREE ? it.len - 1 : it.len - it.ntok + t1;
+        const int hi = !TREE && p.causal ? min(max(pos1 + 1, 0), it.len) : it.len;
         const int lo = p.window > 0 ? min(max(pos0 - p.window + 1, 0), hi) : 0;
         it.all_lo = p.window > 0 ? max(pos1 - p.window + 1, 0) : 0;
-        it.all_hi = p.causal ? min(max(pos0 + 1, 0), it.len) : it.len;
+        it.all_hi = TREE ? max(pos0, 0) : p.causal ? min(max(pos0 + 1, 0), it.len) : it.len;
         const int k0 = lo / BN, nt = (hi + BN - 1) / BN - k0;
         it.parts = sparts == 1 ? 1 : min(sparts, max(1, cdiv_u(nt, chunk)));
         if (it.part >= it.parts)
@@ -292,30 +295,90 @@ __device__ __forceinline__ bool plan_item(const AttnArgs &p, int item, int min_t
     }
 }
 
-// What one query row sees: keys [lo, hi).
-struct AttnRow {
-    int lo, hi;
-    int token, head;        // token of the sequence, head of the group; token < 0: no such row
-};
-
-__device__ __forceinline__ AttnRow attn_row(const AttnArgs &p, const AttnItem &it, int row)
-{
-    AttnRow r;
-    const int token = p.by_group.div(row);
-    r.head = row - token * p.group;
-    r.token = token < it.ntok ? token : -1;
-    const int pos = it.len - it.ntok + token;
-    r.hi = token < it.ntok ? (p.causal ? min(max(pos + 1, 0), it.len) : it.len) : 0;
-    r.lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
-    return r;
-}
-
 // Bits [lo, hi) of 64.
 __device__ __forceinline__ unsigned long long bit_range(int lo, int hi)
 {
     const unsigned long long from = lo <= 0 ? ~0ull : lo >= 64 ? 0ull : ~0ull << lo;
     const unsigned long long upto = hi >= 64 ? ~0ull : hi <= 0 ? 0ull : ~(~0ull << hi);
     return from & upto;
+}
+
+// What one query row sees: keys [lo, hi), and of a tree of drafted tokens
+// (TREE) the context's keys [lo, context) and the nodes, keys context + j, of
+// its bits.
+template <int TREE>
+struct AttnRow {
+    int lo, hi;
+    int token, head;        // token of the sequence, head of the group; token < 0: no such row
+};
+
+template <>
+struct AttnRow<1> {
+    int lo, hi;
+    int token, head;
+    int context;            // keys before the first node; < 0: nodes of keys before the sequence's first
+    const unsigned long long *bits;
+};
+
+template <int TREE>
+__device__ __forceinline__ AttnRow<TREE> attn_row(const AttnArgs &p, const AttnItem &it, int row)
+{
+    AttnRow<TREE> r;
+    const int token = p.by_group.div(row);
+    r.head = row - token * p.group;
+    r.token = token < it.ntok ? token : -1;
+    if constexpr (TREE) {
+        r.hi = token < it.ntok ? it.len : 0;
+        r.lo = 0;
+        r.context = it.len - it.ntok;
+        r.bits = p.mask + (long long)(it.tok0 + max(r.token, 0)) * p.mask_words;
+        if (p.window > 0) {
+            // the node's depth: the nodes that it sees, but for itself
+            int seen = 0;
+            for (int w = 0; w < p.mask_words && 64 * w < it.ntok; ++w)
+                seen += __popcll(r.bits[w] & (it.ntok - 64 * w >= 64 ? ~0ull : ~(~0ull << (it.ntok - 64 * w))));
+            r.lo = min(max(r.context + max(seen - 1, 0) - p.window + 1, 0), max(r.context, 0));
+        }
+    } else {
+        const int pos = it.len - it.ntok + token;
+        r.hi = token < it.ntok ? (p.causal ? min(max(pos + 1, 0), it.len) : it.len) : 0;
+        r.lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
+    }
+    return r;
+}
+
+// The keys key .. key + 63 that a row sees, as bits.
+template <int TREE>
+__device__ __forceinline__ unsigned long long attn_sees(const AttnArgs &p, const AttnRow<TREE> &row, int key)
+{
+    if constexpr (TREE) {
+        unsigned long long see = bit_range(row.lo - key, min(row.context, row.hi) - key);
+        const int node = key - row.context;         // of the first key
+        if (node > -64) {
+            // (whole words; bits past the last word are zeros)
+            const int w = node >> 6, s = node & 63;
+            const unsigned long long a = (unsigned)w < (unsigned)p.mask_words ? row.bits[w] : 0ull;
+            const unsigned long long b = (unsigned)(w + 1) < (unsigned)p.mask_words ? row.bits[w + 1] : 0ull;
+            see |= (s ? a >> s | b << (64 - s) : a) & bit_range(row.context - key, row.hi - key);
+        }
+        return see;
+    } else {
+        return bit_range(row.lo - key, row.hi - key);
+    }
+}
+
+// Whether it sees key k.
+template <int TREE>
+__device__ __forceinline__ bool attn_sees_key(const AttnArgs &p, const AttnRow<TREE> &row, int k)
+{
+    if constexpr (TREE) {
+        const int node = k - row.context;
+        if (node < 0)
+            return k >= row.lo && k < row.hi;
+        return k < row.hi && node >> 6 < p.mask_words && (row.bits[node >> 6] >> (node & 63) & 1);
+    } else {
+        return k >= row.lo && k < row.hi;
+    }
 }
 
 // Rows of codes and scales, and the 16-byte chunks of a row.
@@ -433,8 +496,8 @@ __device__ __forceinline__ bool attn_finite(const float (&f)[8])
 // of the item's keys into its sums f of these columns.  The whole wave looks
 // through 64 keys at a time and takes those that may hold one in turn: once
 // per item, and only where a sum is not finite or a value was replaced.
-template <int F, int D>
-__device__ __forceinline__ void attn_special(const AttnArgs &p, const int *table, const AttnItem &it, const AttnRow &row, int col,
+template <int F, int D, int TREE>
+__device__ __forceinline__ void attn_special(const AttnArgs &p, const int *table, const AttnItem &it, const AttnRow<TREE> &row, int col,
                                              float (&f)[8])
 {
     using G = AttnGeom<F, D>;
@@ -449,7 +512,7 @@ __device__ __forceinline__ void attn_special(const AttnArgs &p, const int *table
             const int i = __ffsll(left) - 1, k = key + i;
             left &= left - 1;
             const long long at = attn_row_at(p, lane_value(page, i), it.head, k);
-            const bool see = k >= row.lo && k < row.hi;
+            const bool see = attn_sees_key<TREE>(p, row, k);
             u2v c;
             if constexpr (F == FMT_FP4)
                 c = u2v{*reinterpret_cast<const unsigned *>(p.codes[1] + at * G::RB + col / 2), 0u};
@@ -553,7 +616,7 @@ __device__ __forceinline__ void attn_write(const AttnArgs &p, const AttnItem &it
 {
     constexpr int RUNS = D / 8;
     const int run = i % RUNS;
-    const AttnRow r = attn_row(p, it, it.row0 + i / RUNS);
+    const AttnRow<0> r = attn_row<0>(p, it, it.row0 + i / RUNS);
     const size_t row = (size_t)(it.tok0 + r.token) * (p.heads * p.group) + it.head * p.group + r.head;
     // (a row that sees no key has l = 0 and sums 0; a NaN is not 0)
     const float inv = s.l == 0.0f ? 0.0f : 1.0f / s.l;
@@ -699,13 +762,13 @@ constexpr int kTileParts = 8;
 // joining alone as above, took 30 us for 31 parts of 64 rows.)
 constexpr int attn_join_blocks(int rows, int dim) { return cdiv_c(rows * dim / 8, 512); }
 
-template <int D, int BM>
+template <int D, int BM, int TREE>
 __global__ __launch_bounds__(256)
 void mx_attn_join(AttnArgs p)
 {
     constexpr int RUNS = D / 8, SUB = attn_join_blocks(BM, D);
     AttnItem it;
-    if (!plan_item<BM, 64, 1>(p, blockIdx.x / SUB, kTileParts, it) || it.parts == 1)
+    if (!plan_item<TREE, BM, 64, 1>(p, blockIdx.x / SUB, kTileParts, it) || it.parts == 1)
         return;
     const int n = min(BM, it.ntok * p.group - it.row0) * RUNS;
 #pragma unroll 1
@@ -748,7 +811,7 @@ void mx_attn_join(AttnArgs p)
 //
 // PAGED: pages of 16 keys or more, so that the two pages of a tile are
 // scalars and the lanes' offsets the same for every tile.
-template <int F, int D, int QT, int PAGED>
+template <int F, int D, int QT, int PAGED, int TREE>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(QT > 1 ? 2 : F == FMT_FP8 && D == 128 ? 3 : 4)))
 void mx_attn_rows(AttnArgs p)
 {
@@ -767,7 +830,7 @@ void mx_attn_rows(AttnArgs p)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 15, g = lane >> 4;
 
     AttnItem it;
-    if (!plan_item<BM, BN>(p, blockIdx.x, 2, it))
+    if (!plan_item<TREE, BM, BN>(p, blockIdx.x, 2, it))
         return;
 
     const int *table = p.table + it.seq * p.table_stride;
@@ -779,11 +842,11 @@ void mx_attn_rows(AttnArgs p)
     auto column = [&](int s) {
         return F == FMT_FP4 ? (D / 4) * g + 8 * s : D == 128 ? (s >> 1) * 64 + 16 * g + 8 * (s & 1) : (D / 4) * g + 8 * s;
     };
-    AttnRow row[QT];
+    AttnRow<TREE> row[QT];
     bf16x8v q[QT][KS];
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-        row[t] = attn_row(p, it, it.row0 + 16 * t + r);
+        row[t] = attn_row<TREE>(p, it, it.row0 + 16 * t + r);
         const uint16_t *src = p.q + (long long)(it.tok0 + max(row[t].token, 0)) * p.q_stride +
                               (long long)(it.head * p.group + row[t].head) * D;
 #pragma unroll
@@ -909,7 +972,7 @@ void mx_attn_rows(AttnArgs p)
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             if (!whole) {
-                const unsigned see = (unsigned)bit_range(row[t].lo - key, row[t].hi - key) & here;
+                const unsigned see = (unsigned)attn_sees<TREE>(p, row[t], key) & here;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     x[t][e >> 2][e & 3] = see >> (4 * g) >> (16 * (e >> 2) + (e & 3)) & 1 ? x[t][e >> 2][e & 3] : -__builtin_inff();
@@ -1029,10 +1092,10 @@ void mx_attn_rows(AttnArgs p)
         const int i = tid + 256 * u;
         if (i - lane >= BM * RUNS)
             continue;
-        const AttnRow at = attn_row(p, it, it.row0 + i / RUNS);
+        const AttnRow<TREE> at = attn_row<TREE>(p, it, it.row0 + i / RUNS);
         // (a row with a NaN among its scores has l = NaN and becomes NaN)
         if (__builtin_expect(__any(at.token >= 0 && fl[u] == fl[u] && (cleans || !attn_finite(f[u]))), 0))
-            attn_special<F, D>(p, table, it, at, i % RUNS * 8, f[u]);
+            attn_special<F, D, TREE>(p, table, it, at, i % RUNS * 8, f[u]);
     }
     static_assert(BYTES >= 40 * 256, "scratch");
     attn_finish<D, BM, 256>(p, it, tid, reinterpret_cast<float *>(lds), [&](int u, AttnSums &out) {
@@ -1106,7 +1169,7 @@ __device__ __forceinline__ TileRange tiles_touching(int key0, int lo, int hi)
     return {a, lo < hi ? max(b - a, 0) : 0};
 }
 
-template <int F, int D, int NW, int PAGED>
+template <int F, int D, int NW, int PAGED, int TREE>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void mx_attn_tile(AttnArgs p)
 {
@@ -1129,7 +1192,7 @@ void mx_attn_tile(AttnArgs p)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 31, h = lane >> 5;
 
     AttnItem it;
-    if (!plan_item<BM, BN>(p, blockIdx.x, kTileParts, it))
+    if (!plan_item<TREE, BM, BN>(p, blockIdx.x, kTileParts, it))
         return;
 
     const int *table = p.table + it.seq * p.table_stride;
@@ -1138,7 +1201,7 @@ void mx_attn_tile(AttnArgs p)
     int entry = T > 0 ? attn_entry(p, table, it.key0 + lane, it.key1) : -1;
     const int chunk = tid % G::CH;                                  // THR is a multiple of CH
 
-    const AttnRow row = attn_row(p, it, it.row0 + 32 * wave + r);
+    const AttnRow<TREE> row = attn_row<TREE>(p, it, it.row0 + 32 * wave + r);
     bf16x8v q[KS];
     {
         const uint16_t *src = p.q + (long long)(it.tok0 + max(row.token, 0)) * p.q_stride +
@@ -1149,7 +1212,7 @@ void mx_attn_tile(AttnArgs p)
     }
     // tiles whose keys every row of the wave sees (of those that are there),
     // and tiles of which some row may see some
-    int lo_most = row.token >= 0 ? row.lo : 0, hi_least = row.token >= 0 ? row.hi : 0x7FFFFFFF;
+    int lo_most = row.token >= 0 ? row.lo : 0, hi_least = row.token >= 0 ? (TREE ? it.all_hi : row.hi) : 0x7FFFFFFF;
     int lo_least = row.token >= 0 ? row.lo : 0x7FFFFFFF, hi_most = row.hi;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -1379,7 +1442,7 @@ void mx_attn_tile(AttnArgs p)
         if (__builtin_expect(!(t > gone && full.has(t)), 0)) {
             const int key = it.key0 + t * BN;
             const unsigned long long there = __ballot(attn_page(p, table, key + lane, it.key1) >= 0);
-            const unsigned long long see = (bit_range(row.lo - key, row.hi - key) & there) >> (4 * h);
+            const unsigned long long see = (attn_sees<TREE>(p, row, key) & there) >> (4 * h);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
                 const unsigned half = e < 16 ? (unsigned)see : (unsigned)(see >> 32);
@@ -1502,7 +1565,7 @@ void mx_attn_tile(AttnArgs p)
         s.l = ml[rr][1];
         // (a row with a NaN among its scores has l = NaN and becomes NaN)
         if (__builtin_expect(__any(i < n && s.l == s.l && (cleans || !attn_finite(s.f))), 0))
-            attn_special<F, D>(p, table, it, attn_row(p, it, it.row0 + rr), i % RUNS * 8, s.f);
+            attn_special<F, D, TREE>(p, table, it, attn_row<TREE>(p, it, it.row0 + rr), i % RUNS * 8, s.f);
         if (i >= n)
             continue;
         if (it.parts == 1)

@@ -486,6 +486,159 @@ int mx_paged_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_str
 size_t mx_paged_attention_workspace_bytes(const mxg_kv_cache_t *cache, int64_t seqs, int64_t tokens,
                                           int64_t q_heads, int64_t max_new);
 
+/*
+ * The position rotation of a step's queries and keys, and its keys and values
+ * into the cache, in one launch: what mx_kv_cache_write does for the rotated
+ * keys and the values, and the rotated queries beside it.  The first `rot`
+ * values of every head of q and k are turned in pairs (a, b), the others kept:
+ *
+ *   a' = a cos - b sin,   b' = b cos + a sin
+ *
+ * for pair i < rot / 2 of values i and i + rot / 2, or (interleaved) 2 i and
+ * 2 i + 1, with cosine and sine of the token's position and i.  The products
+ * are exact and a result is rounded to FP32 and then to BF16.
+ *
+ * q, q_out    BF16, token t at element t * q_stride / t * q_out_stride, its
+ *             [q_heads][head_dim] values contiguous, 16-byte aligned.  q_out is
+ *             q itself (with the same stride: rotated in place) or lies apart
+ *             from it.  q_heads 0: no queries, both may be NULL.
+ * k, v        as for mx_kv_cache_write; k is not written.
+ * slots       as for mx_kv_cache_write.
+ * positions   DEVICE memory, int64 [tokens], 8-byte aligned.  One outside
+ *             [0, table_positions) turns its token's queries and keys to NaN
+ *             (a padding token's, whose slot is -1, reaches nothing by it).
+ * table       FP32 [table_positions][rot / 2][2], cosine and sine; 16-byte
+ *             aligned, table_positions 1 .. 2^31-1.
+ * rot         a multiple of 16, at least 16, at most head_dim.
+ * tokens      >= 0 (0: nothing is enqueued, pointers may be NULL); tokens times
+ *             the larger number of heads, rounded up to a multiple of 4, times
+ *             head_dim at most 2^33.
+ *
+ * MXG_ERR_NULL, MXG_ERR_SHAPE (sizes, q_heads above 65536, a stride below the
+ * heads' values), MXG_ERR_K_ALIGN (head_dim % 32, rot % 16, a stride % 8),
+ * MXG_ERR_CONFIG (interleaved, q_out = q with another stride),
+ * MXG_ERR_PTR_ALIGN, MXG_ERR_DEVICE, MXG_ERR_HIP.
+ */
+int mx_rope_cache_write(const mxg_kv_cache_t *cache, const void *q, void *q_out, const void *k, const void *v,
+                        int64_t q_heads, int64_t q_stride, int64_t q_out_stride, int64_t k_stride, int64_t v_stride,
+                        const int64_t *positions, const int64_t *slots, const float *table, int64_t table_positions,
+                        int64_t rot, int interleaved, int64_t tokens, mxg_stream_t stream);
+
+/*
+ * Attention for trees of drafted tokens: mx_paged_attention for new tokens of
+ * which each sees the sequence's context and some of the other new ones, its
+ * ancestors in a tree of drafts.  The n new tokens of a sequence of L keys are
+ * its nodes; node j is key L - n + j, and the keys before are the context.
+ * Node i sees
+ *
+ *   node j      where bit j % 64 of word j / 64 of its mask is set (itself too)
+ *   context     key j < L - n; with a window > 0 also j > L - n + d - window,
+ *               d the number of nodes that it sees less one, but at least 0:
+ *               its depth.  Nodes are seen whatever the window.
+ *
+ * mask        DEVICE memory, 64-bit words [tokens][mask_words], 8-byte aligned:
+ *             row t that of row t of q.  Bits of nodes that the sequence does
+ *             not have are not looked at; a node past the last word is seen by
+ *             none.
+ * mask_words  1 .. 1024.
+ *
+ * All else, errors included, as for mx_paged_attention (NaN and infinities in
+ * the values of a node that a row does not see do not reach it), and
+ * MXG_ERR_NULL and MXG_ERR_PTR_ALIGN for the mask, MXG_ERR_SHAPE for mask_words.
+ */
+int mx_tree_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, const int32_t *ends,
+                      const int32_t *lens, const int32_t *table, int64_t table_width, const uint64_t *mask,
+                      int64_t mask_words, int64_t seqs, int64_t tokens, int64_t q_heads, int64_t max_new, float scale,
+                      int64_t window, void *out, int out_dtype, float *lse, void *workspace, size_t workspace_bytes,
+                      mxg_stream_t stream);
+/* Workspace bytes mx_tree_attention splits with for these sizes; 0 where it
+ * does not split, or for invalid arguments. */
+size_t mx_tree_attention_workspace_bytes(const mxg_kv_cache_t *cache, int64_t seqs, int64_t tokens,
+                                         int64_t q_heads, int64_t max_new);
+
+/*
+ * Around the grouped product: a router's tokens sorted by expert into its A
+ * operand, the experts' rows back to their tokens, and the gradients of that.
+ * Token t has top_k assignments a = t * top_k + j, each to an expert.
+ *
+ * mx_moe_dispatch writes, for every assignment whose expert is in [0, groups),
+ * token t's row to row pos[a] of y: rows in the order of experts, those of one
+ * expert in the order of a.
+ *
+ * x           BF16 [tokens][K], 16-byte aligned.
+ * experts     DEVICE int64 [tokens][top_k], 8-byte aligned, any content; one
+ *             outside [0, groups) is no expert of this call (another worker's)
+ *             and has no row.  A token may name an expert more than once.
+ * groups      1 .. 1024;  top_k 1 .. 64.
+ * tokens      0 .. 2^24 - 1, tokens * top_k at most 2^26.  With 0 tokens only
+ *             offs is written, and the other pointers may be NULL.
+ * K           at most 2^20, a multiple of 8 (MX kinds 32).
+ * y, y_scale  output.  out_kind MXG_OUT_BF16: y [tokens * top_k][K], y_scale
+ *             ignored.  MXG_OUT_MXFP8 / MXFP4: rows quantized exactly as
+ *             mx_quantize_bf16 does, codes into y, E8M0 codes [..][K/32] into
+ *             y_scale.  Rows past the last expert's end are not written.
+ * offs        output, int32 [groups]: the end row of each expert, as
+ *             mx_grouped_mm_* take it.
+ * pos         output, int32 [tokens][top_k]: the row of each assignment, or -1.
+ * workspace   mx_moe_dispatch_workspace_bytes bytes where that is not 0
+ *             (above 4096 assignments), 16-byte aligned, its first 64 KiB zero
+ *             when it is allocated and left zero by every call: one workspace
+ *             serves these calls, the attention's and the split-K products' of
+ *             a stream, under the rules given for mx_paged_attention.
+ *
+ * MXG_ERR_NULL, MXG_ERR_DTYPE (out_kind), MXG_ERR_SHAPE, MXG_ERR_K_ALIGN,
+ * MXG_ERR_WORKSPACE (none, or too small), MXG_ERR_PTR_ALIGN, MXG_ERR_DEVICE,
+ * MXG_ERR_HIP.
+ */
+int mx_moe_dispatch(const void *x, const int64_t *experts, int64_t tokens, int64_t top_k, int64_t groups, int64_t K,
+                    void *y, void *y_scale, int out_kind, int32_t *offs, int32_t *pos, void *workspace,
+                    size_t workspace_bytes, mxg_stream_t stream);
+size_t mx_moe_dispatch_workspace_bytes(int64_t tokens, int64_t top_k, int64_t groups);
+
+/*
+ * The experts' rows back to their tokens:
+ *
+ *   out[t] = sum_j weights[t][j] * y[pos[t][j]]
+ *
+ * summed in FP32 in the order of j over the assignments whose row is in [0,
+ * rows); a token without one gets zeros.  Without weights it is the gradient of
+ * mx_moe_dispatch (of its BF16 rows).
+ *
+ * y           [rows][N] of y_dtype (BF16, FP16, FP32), 16-byte aligned.
+ * pos         DEVICE int32 [tokens][top_k], any content.
+ * weights     DEVICE FP32 [tokens][top_k], or NULL for ones.
+ * out         [tokens][N] of out_dtype (BF16, FP16, FP32), 16-byte aligned;
+ *             every value is written.
+ * tokens, top_k  as for mx_moe_dispatch.  N a multiple of 8, at most 2^20,
+ *             tokens * N below 2^34; rows 0 .. 2^31 - 1.
+ *
+ * MXG_ERR_NULL, MXG_ERR_DTYPE, MXG_ERR_SHAPE, MXG_ERR_K_ALIGN,
+ * MXG_ERR_PTR_ALIGN, MXG_ERR_DEVICE, MXG_ERR_HIP.
+ */
+int mx_moe_combine(const void *y, int y_dtype, const int32_t *pos, const float *weights, int64_t tokens, int64_t top_k,
+                   int64_t rows, int64_t N, void *out, int out_dtype, mxg_stream_t stream);
+
+/*
+ * The gradients of mx_moe_combine, for d_out [tokens][N]:
+ *
+ *   d_y[pos[t][j]] = weights[t][j] * d_out[t]
+ *   d_weights[t][j] = sum_n d_out[t][n] * y[pos[t][j]][n]     (FP32; 0 without a row)
+ *
+ * d_out, y    of one dtype (BF16, FP16, FP32).
+ * d_y         rows of d_y_kind: that dtype, or MXG_OUT_MXFP8 / MXFP4: rounded
+ *             to BF16 and quantized as mx_quantize_bf16 does, codes into d_y and
+ *             scales into d_y_scale [rows][N/32]: the A operand of the backward
+ *             products (N a multiple of 32).  Rows that no assignment has are not
+ *             written; the rows of pos that lie in [0, rows) are distinct (of
+ *             two assignments with one row either's gradient may be left there).
+ * d_weights   FP32 [tokens][top_k], or NULL: not computed, and y not read.
+ *
+ * All else as for mx_moe_combine.
+ */
+int mx_moe_combine_grad(const void *d_out, const void *y, int dtype, const int32_t *pos, const float *weights,
+                        int64_t tokens, int64_t top_k, int64_t rows, int64_t N, void *d_y, void *d_y_scale,
+                        int d_y_kind, float *d_weights, mxg_stream_t stream);
+
 /* The configuration the default entry points pick for a shape: returns the
  * variant (>= 0) and stores the K-part count in *splits (if not NULL), for
  * a call given a large enough workspace (with_workspace = 1) or none (0);
