@@ -100,6 +100,7 @@ struct AttnArgs {
     float per_target;                       // KV heads / workgroups that can run at once
     const unsigned long long *mask;         // trees of drafted tokens: [tokens][mask_words], the nodes that each sees
     int mask_words;
+    int resident;                           // (trees) workgroups that can run at once
 };
 
 // One workgroup's work.
@@ -195,6 +196,43 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &p, int s, int &carry
 
 __device__ __forceinline__ int cdiv_u(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1u) / (unsigned)b); }
 
+// Trees: the smallest chunk, from `least` on, with which all items run at
+// once.  (Chunks of the average work make up to one item per row tile more
+// than run at once, and those few are a second round: two sequences of 61 and
+// 40 nodes over 131072 and 81000 keys, 272 items of 256 rows for 256
+// workgroups, took 650 us, and in one round 400.)  Where the row tiles alone are
+// too many for that, or it would leave the workgroups half idle: the average
+// work, which cuts none of like sequences, or half of it where some sequence
+// has far more (32 sequences of 100 to 16000 keys 85 us instead of 90).
+__device__ __forceinline__ int one_round(const AttnArgs &p, const AttnSeq &q, float total, int least)
+{
+    // (least is half of the average work)
+    if (p.seqs > 64)
+        return least;
+    const int rounds = __any(q.ktiles > 4 * least) ? least : 2 * least;
+    const int last = p.seqs > 1 ? 63 : 0;
+    int tiles = p.heads * q.rtiles;
+    if (p.seqs > 1)
+        tiles = wave_prefix(tiles);
+    tiles = lane_value(tiles, last);
+    if (tiles == 0 || tiles >= p.resident)
+        return rounds;
+    const float even = total * (float)p.heads / (float)p.resident;
+    int a = max(uniform((int)fminf(even, 1e9f)), least);
+    int b = max(uniform((int)fminf(total * (float)p.heads / (float)(p.resident - tiles), 1e9f)) + 2, a);
+    for (int i = 0; a < b && i < 8; ++i) {
+        const int c = (a + b) >> 1;
+        int items = p.heads * q.rtiles * max(1, cdiv_u(q.ktiles, c));
+        if (p.seqs > 1)
+            items = wave_prefix(items);
+        if (lane_value(items, last) <= p.resident)
+            b = c;
+        else
+            a = c + 1;
+    }
+    return (float)b <= 1.7f * even ? b : rounds;
+}
+
 // Find item `item` of the launch; false if there is none.  Every wave of the
 // workgroup computes it (all results are wave-uniform).  min_tiles: the
 // fewest key tiles worth a part of their own.  JOIN: one item per row tile
@@ -222,8 +260,10 @@ __device__ __forceinline__ bool plan_item(const AttnArgs &p, int item, int min_t
         }
         if (p.seqs > 1)
             total = wave_prefix(total);
-        total = __int_as_float(lane_value(__float_as_int(total), p.seqs > 1 ? 63 : 0)) * p.per_target * 1.001f;
-        chunk = max(uniform((int)fminf(total, 1e9f) + 1), min_tiles);
+        total = __int_as_float(lane_value(__float_as_int(total), p.seqs > 1 ? 63 : 0));
+        chunk = max(uniform((int)fminf(total * p.per_target * 1.001f, 1e9f) + 1), min_tiles);
+        if constexpr (TREE)
+            chunk = one_round(p, q, total, chunk);
     }
     carry = carry64;
     int slots = 0, tiles = 0;                         // before the 64 sequences looked at
@@ -652,31 +692,111 @@ __device__ __forceinline__ void attn_put_part(__amdgpu_buffer_rsrc_t slot, int i
                                               (unsigned)(SUMS + i / RUNS * 8), 0, kDeviceScope);
 }
 
-// Parts first, first + step, .. of run i, in that order.
+// Parts first, first + step, .. below `end` of run i, in that order.
 template <int D, int NR>
-__device__ __forceinline__ void attn_sum_parts(const AttnArgs &p, const AttnItem &it, int i, int first, int step, AttnSums &s)
+__device__ __forceinline__ void attn_sum_parts(const AttnArgs &p, const AttnItem &it, int i, int first, int step, int end, AttnSums &s)
 {
     constexpr int RUNS = D / 8, SUMS = NR * D * 4;
     s.clear();
     constexpr int PF = 8;       // parts in flight
-    for (int q0 = first; q0 < it.parts; q0 += PF * step) {
+    for (int q0 = first; q0 < end; q0 += PF * step) {
         u4v a[PF], b[PF];
         u2v ml[PF];
 #pragma unroll
         for (int q = 0; q < PF; ++q) {
-            const __amdgpu_buffer_rsrc_t src = attn_slot<D, NR>(p, it, min(q0 + q * step, it.parts - 1));
+            const __amdgpu_buffer_rsrc_t src = attn_slot<D, NR>(p, it, min(q0 + q * step, end - 1));
             ml[q] = __builtin_amdgcn_raw_buffer_load_b64(src, (unsigned)(SUMS + i / RUNS * 8), 0, kDeviceScope);
             a[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(i * 32), 0, kDeviceScope);
             b[q] = __builtin_amdgcn_raw_buffer_load_b128(src, (unsigned)(i * 32 + 16), 0, kDeviceScope);
         }
 #pragma unroll
         for (int q = 0; q < PF; ++q)
-            if (q0 + q * step < it.parts) {
+            if (q0 + q * step < end) {
                 const v4f fa = __builtin_bit_cast(v4f, a[q]), fb = __builtin_bit_cast(v4f, b[q]);
                 s.add({fa[0], fa[1], fa[2], fa[3], fb[0], fb[1], fb[2], fb[3]}, __uint_as_float(ml[q][0]),
                       __uint_as_float(ml[q][1]));
             }
     }
+}
+
+// Trees: the join of a row tile's parts, n runs of it, once this workgroup's
+// are in its slot: by the workgroup that arrives last.  More than 2 kJoin
+// parts are joined in two steps, kJoin of them by the last of each kJoin and
+// what these leave by the last of all (one sequence of 4 nodes over 16000 keys,
+// 63 parts for each of 8 heads: 29.7 us by one alone, 17.5 in two steps).
+constexpr int kJoin = 8;
+constexpr int kTreeTiles = 8192;        // row tiles that may be split, and as many slots
+
+template <int D, int NR, int NTHR>
+__device__ __forceinline__ void attn_join_tree(const AttnArgs &p, const AttnItem &it, int tid, int n, float *scratch)
+{
+    __shared__ unsigned arrived;
+    auto last = [&](int counter, int of) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        if (tid == 0) {
+            arrived = __hip_atomic_fetch_add(p.counters + counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (arrived == (unsigned)(of - 1))
+                __hip_atomic_store(p.counters + counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        return arrived == (unsigned)(of - 1);
+    };
+    // parts first, first + step, .. below end, to the outputs or to part `to`
+    auto sum = [&](int first, int step, int end, int to) {
+        auto put = [&](int i, AttnSums &s) {
+            if (to < 0)
+                attn_write<D>(p, it, i, s);
+            else
+                attn_put_part<D, NR>(attn_slot<D, NR>(p, it, to), i, s);
+        };
+        const int groups = n <= NTHR / 4 ? 4 : n <= NTHR / 2 ? 2 : 1;
+        if (groups > 1) {
+            // (whole waves per group)
+            const int each = NTHR / groups, group = uniform(tid / each), i = tid - group * each;
+            AttnSums s;
+            if (i < n) {
+                attn_sum_parts<D, NR>(p, it, i, first + group * step, step * groups, end, s);
+                if (group > 0) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        scratch[e * NTHR + tid] = s.f[e];
+                    scratch[8 * NTHR + tid] = s.m;
+                    scratch[9 * NTHR + tid] = s.l;
+                }
+            }
+            __syncthreads();
+            if (group == 0 && i < n) {
+                for (int o = 1; o < groups; ++o) {
+                    const float *src = scratch + o * each + i;
+                    s.add({src[0], src[NTHR], src[2 * NTHR], src[3 * NTHR], src[4 * NTHR], src[5 * NTHR], src[6 * NTHR], src[7 * NTHR]},
+                          src[8 * NTHR], src[9 * NTHR]);
+                }
+                put(i, s);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = tid; i < n; i += NTHR) {
+                AttnSums s;
+                attn_sum_parts<D, NR>(p, it, i, first, step, end, s);
+                put(i, s);
+            }
+        }
+    };
+    if (it.parts <= 2 * kJoin) {
+        if (last(it.counter, it.parts))
+            sum(0, 1, it.parts, -1);
+        return;
+    }
+    const int from = it.part / kJoin * kJoin, upto = min(from + kJoin, it.parts);
+    if (upto > from + 1) {
+        // (the counters behind the row tiles', by the slot of the first of them)
+        if (!last(kTreeTiles + it.slot + from * it.slot_step, upto - from))
+            return;
+        sum(from, 1, upto, from);
+    }
+    if (last(it.counter, (it.parts + kJoin - 1) / kJoin))
+        sum(0, kJoin, it.parts, -1);
 }
 
 // The end of a part of a row tile of few rows, of which run u of thread `tid`
@@ -690,7 +810,7 @@ __device__ __forceinline__ void attn_sum_parts(const AttnArgs &p, const AttnItem
 // these leave threads over, two or four groups of threads take every second
 // or fourth part each and are joined in `scratch` (40 NTHR bytes of LDS that
 // nothing else uses any more).
-template <int D, int NR, int NTHR, class Get>
+template <int D, int NR, int NTHR, int TREE, class Get>
 __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &it, int tid, float *scratch, Get &&get)
 {
     constexpr int RUNS = D / 8, NU = cdiv_c(NR * RUNS, NTHR);
@@ -708,6 +828,10 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
         }
     if (it.parts == 1)
         return;
+    if constexpr (TREE) {
+        attn_join_tree<D, NR, NTHR>(p, it, tid, n, scratch);
+        return;
+    }
     __shared__ unsigned arrived;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
@@ -722,7 +846,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
         const int each = NTHR / groups, group = uniform(tid / each), i = tid - group * each;
         AttnSums s;
         if (i < n) {
-            attn_sum_parts<D, NR>(p, it, i, group, groups, s);
+            attn_sum_parts<D, NR>(p, it, i, group, groups, it.parts, s);
             if (group > 0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -744,7 +868,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
 #pragma unroll 1
         for (int i = tid; i < n; i += NTHR) {
             AttnSums s;
-            attn_sum_parts<D, NR>(p, it, i, 0, 1, s);
+            attn_sum_parts<D, NR>(p, it, i, 0, 1, it.parts, s);
             attn_write<D>(p, it, i, s);
         }
     }
@@ -776,7 +900,7 @@ void mx_attn_join(AttnArgs p)
         const int i = (blockIdx.x % SUB * 2 + u) * 256 + threadIdx.x;
         if (i < n) {
             AttnSums s;
-            attn_sum_parts<D, BM>(p, it, i, 0, 1, s);
+            attn_sum_parts<D, BM>(p, it, i, 0, 1, it.parts, s);
             attn_write<D>(p, it, i, s);
         }
     }
@@ -1098,7 +1222,7 @@ void mx_attn_rows(AttnArgs p)
             attn_special<F, D, TREE>(p, table, it, at, i % RUNS * 8, f[u]);
     }
     static_assert(BYTES >= 40 * 256, "scratch");
-    attn_finish<D, BM, 256>(p, it, tid, reinterpret_cast<float *>(lds), [&](int u, AttnSums &out) {
+    attn_finish<D, BM, 256, TREE>(p, it, tid, reinterpret_cast<float *>(lds), [&](int u, AttnSums &out) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             out.f[e] = f[u][e];

@@ -101,6 +101,7 @@ struct AttnPlan {
     int64_t base[2];        // most row tiles
     int target[2];          // parts
     size_t bytes[2];        // of the workspace for splitting; 0: none
+    int resident;           // (trees) workgroups that can run at once
 };
 
 AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, int64_t dim, int64_t max_new)
@@ -135,6 +136,46 @@ AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
         const bool whole = seqs == 1 && heads * cdiv(tokens * group, bm) >= p.target[i];
         p.bytes[i] = p.base[i] <= kSplitCounters && !whole ? (size_t)2 * p.target[i] * attn_slot_bytes(bm, (int)dim) : 0;
     }
+    return p;
+}
+
+// Trees: one launch, whatever the sequences' numbers of nodes.  keys: the most
+// keys of a sequence, as far as the host knows.
+//
+// Rows per tile, by the work: `tiles` of 32 rows (all heads) times keys, and
+// rows of a sequence on average.  Few rows per tile have more parts that run
+// side by side, many read and expand a key less often.  us, 8 KV heads of 128
+// with 4 query heads each, E4M3:
+//                                               16    32   128   256 rows
+//     1 sequence of 27 nodes over 1051 keys    12.7  14.9    27    28
+//     1 of 16 over 4112                        16.5  23.5    27    29
+//     32 of 16 over 256                        18.5  15.0    18    22
+//     1 of 64 over 16064                         51    40    54    56
+//     32 of 16 over 100 to 16000                112    85    90   151
+//     8 of 64 over 4096                          92    57    62    65
+//     32 of 32 over 4096                        181   118   112   128
+//     1 of 200 over 16200                       165   108    87    84
+//     32 of 64 over 4096                        344   230   171   152
+AttnPlan tree_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, int64_t dim, int64_t max_new, int64_t keys)
+{
+    AttnPlan p = {};
+    const int64_t some = std::min(seqs, tokens);        // sequences with a node
+    const int64_t rows = tokens * group, mean = cdiv(rows, std::max<int64_t>(some, 1)), tiles = heads * cdiv(rows, 32);
+    p.n = 1;
+    p.which[0] = max_new * group <= 16 || (tiles * keys < 400000 && heads * cdiv(rows, 16) <= 512) ? ROWS_16
+                 : mean <= 64 || tiles * keys < 2500000                                           ? ROWS_32
+                 : mean <= 128                                                                    ? ROWS_128
+                                                                                                  : ROWS_256;
+    const int bm = kAttnBM[p.which[0]];
+    p.upto[0] = INT32_MAX;
+    p.base[0] = heads * (rows / bm + some);
+    // (one_round: items that run at once, or twice as many.  With 768 instead of
+    // 512 the parts' joins cost more than the parts gain: 1 sequence of 27 nodes
+    // over 16027 keys 40 us instead of 31; with 256, 1 of 200 over
+    // 4296 48 instead of 43)
+    p.resident = p.which[0] == ROWS_256 ? 256 : 512;
+    p.target[0] = 2 * p.resident;
+    p.bytes[0] = p.base[0] <= kTreeTiles ? (size_t)2 * p.target[0] * attn_slot_bytes(bm, (int)dim) : 0;
     return p;
 }
 
@@ -185,7 +226,9 @@ int run_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, 
     if ((uintptr_t)mask & 7)
         return MXG_ERR_PTR_ALIGN;
     const int64_t group = q_heads / cache->kv_heads;
-    const AttnPlan plan = attn_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new);
+    const AttnPlan plan = TREE ? tree_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new,
+                                           std::min<int64_t>(table_width * cache->page_size, window > 0 ? window + max_new : INT32_MAX))
+                               : attn_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new);
     for (int i = 0; i < plan.n; ++i)        // (split ones are far below)
         if (plan.base[i] > kMaxThreads / kAttnThreads[plan.which[i]])
             return MXG_ERR_SHAPE;
@@ -229,6 +272,7 @@ int run_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, 
         a.rows_above = plan.above[i];
         a.rows_upto = plan.upto[i];
         a.per_target = (float)a.heads / (float)plan.target[i];
+        a.resident = plan.resident;
         const int64_t grid = plan.base[i] + (parts ? plan.target[i] : 0);
         hipLaunchKernelGGL(attn_fn<TREE>(which, cache->is_fp4 != 0, cache->head_dim, cache->page_size), dim3((unsigned)grid),
                            dim3(kAttnThreads[which]), 0, (hipStream_t)stream, a);

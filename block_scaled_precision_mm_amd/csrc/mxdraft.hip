@@ -105,7 +105,12 @@ size_t mx_tree_attention_workspace_bytes(const mxg_kv_cache_t *cache, int64_t se
 {
     if (validate_cache(cache) || !attn_shape_ok(cache, seqs, tokens, q_heads, max_new))
         return 0;
-    return attn_workspace(attn_plan(seqs, tokens, cache->kv_heads, q_heads / cache->kv_heads, cache->head_dim, max_new));
+    // (for any number of keys)
+    const int64_t group = q_heads / cache->kv_heads;
+    size_t most = 0;
+    for (const int64_t keys : {(int64_t)0, (int64_t)1 << 30})
+        most = std::max(most, attn_workspace(tree_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new, keys)));
+    return most;
 }
 
 int mx_tree_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, const int32_t *ends,
