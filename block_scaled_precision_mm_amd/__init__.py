@@ -771,15 +771,17 @@ def _int32(name, t, shape, dev):
         raise ValueError("%s must be a contiguous int32 CUDA tensor of shape %s on the current device" % (name, tuple(shape)))
 
 
-def _attention(name, fn, need_fn, cache, q, ends, lens, table, out, lse, scale, window, max_new, workspace, stream, mask,
-               causal):
-    """mx_paged_attention, or with a mask mx_tree_attention."""
+_F32, _I32, _I64T = torch.float32, torch.int32, torch.int64
+
+
+def _attention_args(cache, q, ends, lens, table, out, lse):
+    """The checks of an attention call's tensors: device, sequences, q's shape and stride between tokens, out's kind."""
     tokens, heads, dim = q.shape
-    seqs = ends.shape[0]
     if dim != cache.head_dim:
         raise ValueError("q has head_dim %d, the cache %d" % (dim, cache.head_dim))
     dev = _cache_device(cache)
     qs = _token_rows("q", q, tokens, heads, dim, dev)
+    seqs = ends.shape[0]
     _int32("ends", ends, (seqs,), dev)
     _int32("lens", lens, (seqs,), dev)
     if table.dim() != 2:
@@ -788,23 +790,10 @@ def _attention(name, fn, need_fn, cache, q, ends, lens, table, out, lse, scale, 
     kind = _OUT_OF_DTYPE.get(out.dtype)
     if kind is None or out.get_device() != dev or out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous CUDA tensor of q's shape in BF16, FP16 or FP32 on the current device")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (tokens, heads) or
+    if lse is not None and (lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != (tokens, heads) or
                             not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 CUDA tensor [tokens][q_heads] on the current device")
-    if max_new is None:
-        max_new = tokens
-    scale = dim ** -0.5 if scale is None else scale
-    need = need_fn(cache._ref, seqs, tokens, heads, max_new) if workspace is not None else 0
-    head = (cache._ref, q.data_ptr(), qs, ends.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1])
-    if mask is None:
-        middle = (seqs, tokens, heads, max_new, scale, int(causal), window)
-    else:
-        if mask.dtype is not torch.int64 or mask.get_device() != dev or mask.dim() != 2 or mask.shape[0] != tokens or \
-                not mask.is_contiguous():
-            raise ValueError("mask must be a contiguous int64 CUDA tensor [tokens][words] on the current device")
-        middle = (mask.data_ptr(), mask.shape[1], seqs, tokens, heads, max_new, scale, window)
-    _call(name, fn, head + middle + (out.data_ptr(), kind, 0 if lse is None else lse.data_ptr()), workspace, need, dev,
-          _stream(stream, dev))
+    return dev, seqs, tokens, heads, dim, qs, kind
 
 
 def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, causal=True, window=0,
@@ -815,8 +804,14 @@ def mx_paged_attention(cache, q, ends, lens, table, out, lse=None, scale=None, c
     sequence]; out contiguous [tokens][q_heads][head_dim] in BF16 / FP16 /
     FP32; lse float32 [tokens][q_heads] or None.  scale: 1/sqrt(head_dim) if
     None; max_new: the most new tokens of a sequence, if known (for speed)."""
-    _attention("mx_paged_attention", _lib.mx_paged_attention, _lib.mx_paged_attention_workspace_bytes, cache, q, ends,
-               lens, table, out, lse, scale, window, max_new, workspace, stream, None, causal)
+    dev, seqs, tokens, heads, dim, qs, kind = _attention_args(cache, q, ends, lens, table, out, lse)
+    if max_new is None:
+        max_new = tokens
+    need = _lib.mx_paged_attention_workspace_bytes(cache._ref, seqs, tokens, heads, max_new) if workspace is not None else 0
+    _call("mx_paged_attention", _lib.mx_paged_attention,
+          (cache._ref, q.data_ptr(), qs, ends.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1], seqs,
+           tokens, heads, max_new, dim ** -0.5 if scale is None else scale, int(causal), window, out.data_ptr(),
+           kind, 0 if lse is None else lse.data_ptr()), workspace, need, dev, _stream(stream, dev))
 
 
 def paged_attention(cache, q, ends, lens, table, out_dtype=torch.bfloat16, stream=None, **kw) -> torch.Tensor:
@@ -839,10 +834,17 @@ def mx_tree_attention(cache, q, ends, lens, table, mask, out, lse=None, scale=No
     of a token's row set where it sees the j-th new token of its sequence,
     itself included (tree_mask makes it from parents); all else as for
     mx_paged_attention."""
-    if mask is None:
+    dev, seqs, tokens, heads, dim, qs, kind = _attention_args(cache, q, ends, lens, table, out, lse)
+    if mask is None or mask.dtype is not _I64T or mask.get_device() != dev or mask.dim() != 2 or mask.shape[0] != tokens or \
+            not mask.is_contiguous():
         raise ValueError("mask must be a contiguous int64 CUDA tensor [tokens][words] on the current device")
-    _attention("mx_tree_attention", _lib.mx_tree_attention, _lib.mx_tree_attention_workspace_bytes, cache, q, ends, lens,
-               table, out, lse, scale, window, max_new, workspace, stream, mask, False)
+    if max_new is None:
+        max_new = tokens
+    need = _lib.mx_tree_attention_workspace_bytes(cache._ref, seqs, tokens, heads, max_new) if workspace is not None else 0
+    _call("mx_tree_attention", _lib.mx_tree_attention,
+          (cache._ref, q.data_ptr(), qs, ends.data_ptr(), lens.data_ptr(), table.data_ptr(), table.shape[1], mask.data_ptr(),
+           mask.shape[1], seqs, tokens, heads, max_new, dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+           kind, 0 if lse is None else lse.data_ptr()), workspace, need, dev, _stream(stream, dev))
 
 
 def tree_attention(cache, q, ends, lens, table, mask, out_dtype=torch.bfloat16, stream=None, **kw) -> torch.Tensor:
@@ -923,13 +925,15 @@ def mx_moe_dispatch_workspace_bytes(tokens, top_k, groups) -> int:
     return int(_lib.mx_moe_dispatch_workspace_bytes(tokens, top_k, groups))
 
 
-def _rows(name, t, rows, width, dev, dtype=None):
-    """A contiguous [rows][width] CUDA tensor (of rows, if given)."""
-    if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows) or t.get_device() != dev or \
-            not t.is_contiguous() or (dtype is not None and t.dtype is not dtype):
-        raise ValueError("%s must be a contiguous %sCUDA tensor [%s][%d] on the current device"
-                         % (name, "" if dtype is None else "%s " % str(dtype).replace("torch.", ""),
-                            "rows" if rows is None else rows, width))
+def _rows(name, t, rows, width, dev):
+    """A contiguous [rows][width] CUDA tensor."""
+    if t.shape != (rows, width) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor [%d][%d] on the current device" % (name, rows, width))
+
+
+def _of_type(name, t, dtype):
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s" % (name, str(dtype).replace("torch.", "")))
 
 
 def _mx_kind(name, y, y_scale, rows, width, dev):
@@ -955,7 +959,8 @@ def mx_moe_dispatch(x, experts, y, y_scale, offs, pos, workspace="auto", stream=
     offs int32 [groups] and pos int32 [tokens][top_k] are written."""
     dev = _here()
     tokens, K = x.shape
-    _rows("x", x, tokens, K, dev, _BF16)
+    _rows("x", x, tokens, K, dev)
+    _of_type("x", x, _BF16)
     if experts.dim() != 2 or offs.dim() != 1:
         raise ValueError("experts must be [tokens][top_k] and offs [groups]")
     top_k, groups = experts.shape[1], offs.shape[0]
@@ -995,7 +1000,8 @@ def _combine_args(pos, weights, dev):
     tokens, top_k = pos.shape
     _int32("pos", pos, (tokens, top_k), dev)
     if weights is not None:
-        _rows("weights", weights, tokens, top_k, dev, torch.float32)
+        _rows("weights", weights, tokens, top_k, dev)
+        _of_type("weights", weights, _F32)
     return tokens, top_k, 0 if weights is None else weights.data_ptr()
 
 
@@ -1049,11 +1055,13 @@ def mx_moe_combine_grad(d_out, y, pos, weights, d_y, d_y_scale=None, d_weights=N
     else:
         raise ValueError("d_y must be of d_out's type, or 1-byte codes with scales")
     if d_weights is not None:
-        _rows("d_weights", d_weights, tokens, top_k, dev, torch.float32)
+        _rows("d_weights", d_weights, tokens, top_k, dev)
+        _of_type("d_weights", d_weights, _F32)
         if y is None:
             raise ValueError("y is needed for d_weights")
     if y is not None:
-        _rows("y", y, rows, N, dev, d_out.dtype)
+        _rows("y", y, rows, N, dev)
+        _of_type("y", y, d_out.dtype)
     st = _lib.mx_moe_combine_grad(d_out.data_ptr(), 0 if y is None else y.data_ptr(), dtype, pos.data_ptr(), pw, tokens, top_k,
                                   rows, N, d_y.data_ptr(), 0 if kind == dtype else d_y_scale.data_ptr(), kind,
                                   0 if d_weights is None else d_weights.data_ptr(), _stream(stream, dev))

@@ -8,6 +8,11 @@
 //     a' = a cos - b sin,   b' = b cos + a sin
 // with cosine and sine of (position, i) from a table that the caller keeps.
 //
+// Bound: HBM for many tokens: 8191 of 32 query and 8 key heads of 128 into
+// E4M3 move 189 MB in 36.6 us, 5.2 TB/s, what a large copy reaches.  For a
+// step's few the launch and a chain of dependent accesses (position, angles,
+// slot): 64 tokens 2.9 us.
+//
 // Roundings.  A BF16 value times an FP32 one is exact in FP64, so each result
 // is rounded there once, then to FP32 and to BF16: it does not depend on how
 // products are contracted, and the keys' codes are those of mx_kv_cache_write
@@ -20,7 +25,7 @@
 namespace mxg {
 
 struct RopeArgs {
-    CacheArgs kv;               // in: keys and values; n: 8-value pieces of one head each of kHeads, all tokens
+    CacheArgs kv;               // in: keys and values; n: 8-value pieces, one for each group of heads
     const uint16_t *q;
     uint16_t *q_out;            // may be q
     long long q_stride, q_out_stride;
@@ -28,15 +33,38 @@ struct RopeArgs {
     const float *table;         // [npositions][rot / 2] (cosine, sine)
     long long npositions;
     int units;                  // of queries: tokens * q_groups * dim / 16
-    int q_heads, q_groups, kv_groups;       // heads, and groups of at most kRopeHeads of them
+    int q_heads, q_groups, kv_groups;       // heads, and groups of at most H of them
     FastDiv per_token, per_group;           // units of a token, of a group (queries)
     FastDiv kv_token, kv_group;             // pieces of a token, of a group (keys, values)
     int rot, q_blocks, kv_blocks;           // workgroups of queries, of keys (as many of values)
 };
 
-// Heads of a token per thread, all their loads in flight together and the
-// angles loaded once for them.
+// H heads of a token per thread (every q_groups-th), all their loads in flight
+// together and the angles loaded once for them.  One head for few tokens, whose
+// time is one thread's; four for many, and then past the caches, as nothing
+// of a prompt's queries stays there until they are read (us, 32 and 8 heads of
+// 128; with one head 1000 tokens 6.6 both ways):
+//     tokens           64    512   1000   2000   4000   8000
+//     1 head          2.9    4.4    6.6   11.1   22.9   41.1
+//     4 heads         4.4    5.1    6.6    9.9   19.1   35.8
 constexpr int kRopeHeads = 4;
+
+template <int H>
+__device__ __forceinline__ u4v rope_load(const uint16_t *at)
+{
+    const u4v *v = reinterpret_cast<const u4v *>(at);
+    return H > 1 ? __builtin_nontemporal_load(v) : *v;
+}
+
+template <int H>
+__device__ __forceinline__ void rope_store(uint16_t *at, u4v w)
+{
+    u4v *v = reinterpret_cast<u4v *>(at);
+    if constexpr (H > 1)
+        __builtin_nontemporal_store(w, v);
+    else
+        *v = w;
+}
 
 // (cos, sin) of the eight pairs 8u .. of a position, NaN for one that the table
 // does not have.
@@ -107,7 +135,7 @@ __device__ __forceinline__ u4v rope_seconds(u4v a, u4v b, const RopeAngles &t)
 // u + rot / 16, or (interleaved, and past the rotated values) pieces 2u and
 // 2u + 1, of every q_groups-th head.  Both pieces of a pair are one thread's,
 // so q may be rotated in place.
-template <int INTER>
+template <int INTER, int H>
 __device__ __forceinline__ void rope_queries(const RopeArgs &p)
 {
     const int n = (int)blockIdx.x * 256 + (int)threadIdx.x;
@@ -121,18 +149,18 @@ __device__ __forceinline__ void rope_queries(const RopeArgs &p)
     const uint16_t *src = p.q + t * p.q_stride;
     uint16_t *dst = p.q_out + t * p.q_out_stride;
     const long long position = p.positions[t];
-    u4v a[kRopeHeads], b[kRopeHeads];
+    u4v a[H], b[H];
 #pragma unroll
-    for (int j = 0; j < kRopeHeads; ++j) {
+    for (int j = 0; j < H; ++j) {
         const int head = min(group + j * p.q_groups, p.q_heads - 1);
-        a[j] = *reinterpret_cast<const u4v *>(src + head * dim + first);
-        b[j] = *reinterpret_cast<const u4v *>(src + head * dim + second);
+        a[j] = rope_load<H>(src + head * dim + first);
+        b[j] = rope_load<H>(src + head * dim + second);
     }
     if (turned) {
         RopeAngles w;
         w.load(p, position, u);
 #pragma unroll
-        for (int j = 0; j < kRopeHeads; ++j) {
+        for (int j = 0; j < H; ++j) {
             if (INTER) {
                 a[j] = rope_adjacent(a[j], w, 0);
                 b[j] = rope_adjacent(b[j], w, 4);
@@ -144,11 +172,11 @@ __device__ __forceinline__ void rope_queries(const RopeArgs &p)
         }
     }
 #pragma unroll
-    for (int j = 0; j < kRopeHeads; ++j) {
+    for (int j = 0; j < H; ++j) {
         const int head = group + j * p.q_groups;
         if (head < p.q_heads) {
-            *reinterpret_cast<u4v *>(dst + head * dim + first) = a[j];
-            *reinterpret_cast<u4v *>(dst + head * dim + second) = b[j];
+            rope_store<H>(dst + head * dim + first, a[j]);
+            rope_store<H>(dst + head * dim + second, b[j]);
         }
     }
 }
@@ -157,7 +185,7 @@ __device__ __forceinline__ void rope_queries(const RopeArgs &p)
 // the four lanes of a quad have a block of 32.  A key's piece takes the values
 // that it is paired with from memory as well (a second time from the cache of
 // the CU), so that blocks need not match pairs.
-template <int F, int INTER>
+template <int F, int INTER, int H>
 __device__ __forceinline__ void rope_keys(const RopeArgs &p, int kv, int block)
 {
     const int n = block * 256 + (int)threadIdx.x;
@@ -171,9 +199,9 @@ __device__ __forceinline__ void rope_keys(const RopeArgs &p, int kv, int block)
     const uint16_t *src = p.kv.in[kv] + t * p.kv.stride[kv];
     const long long slot = mine ? p.kv.slots[t] : -1;
     const long long position = turned ? p.positions[t] : 0;
-    u4v a[kRopeHeads], b[kRopeHeads];
+    u4v a[H], b[H];
 #pragma unroll
-    for (int j = 0; j < kRopeHeads; ++j) {
+    for (int j = 0; j < H; ++j) {
         const int head = min(group + j * p.kv_groups, p.kv.heads - 1);
         a[j] = *reinterpret_cast<const u4v *>(src + head * dim + 8 * piece);
         if (!INTER)
@@ -183,7 +211,7 @@ __device__ __forceinline__ void rope_keys(const RopeArgs &p, int kv, int block)
         RopeAngles w;
         w.load(p, position, INTER ? piece >> 1 : second ? piece - half : piece);
 #pragma unroll
-        for (int j = 0; j < kRopeHeads; ++j) {
+        for (int j = 0; j < H; ++j) {
             if (INTER) {
                 RopeAngles v = w;
                 if (piece & 1)
@@ -199,7 +227,7 @@ __device__ __forceinline__ void rope_keys(const RopeArgs &p, int kv, int block)
         }
     }
 #pragma unroll
-    for (int j = 0; j < kRopeHeads; ++j) {
+    for (int j = 0; j < H; ++j) {
         const int head = group + j * p.kv_groups;
         const unsigned s = mx_scale_code<F>(quad_max(amax8(a[j])));
         const u2v c = mx_encode8<F>(a[j], s);
@@ -215,17 +243,17 @@ __device__ __forceinline__ void rope_keys(const RopeArgs &p, int kv, int block)
     }
 }
 
-template <int F, int INTER>
+template <int F, int INTER, int H>
 __global__ __launch_bounds__(256)
 void mx_rope_write(RopeArgs p)
 {
     const int block = blockIdx.x;
     if (block < p.q_blocks)
-        rope_queries<INTER>(p);
+        rope_queries<INTER, H>(p);
     else if (block < p.q_blocks + p.kv_blocks)
-        rope_keys<F, INTER>(p, 0, block - p.q_blocks);
+        rope_keys<F, INTER, H>(p, 0, block - p.q_blocks);
     else
-        rope_keys<F, INTER>(p, 1, block - p.q_blocks - p.kv_blocks);
+        rope_keys<F, INTER, H>(p, 1, block - p.q_blocks - p.kv_blocks);
 }
 
 }  // namespace mxg

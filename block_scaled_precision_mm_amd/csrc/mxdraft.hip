@@ -11,8 +11,14 @@ using namespace mxg;
 
 namespace {
 
-// Heads in groups of at most kRopeHeads: how many groups.
-int64_t head_groups(int64_t heads) { return cdiv(heads, kRopeHeads); }
+typedef void (*RopeFn)(RopeArgs);
+
+template <int H>
+RopeFn rope_fn(bool fp4, bool interleaved)
+{
+    return fp4 ? (interleaved ? &mx_rope_write<FMT_FP4, 1, H> : &mx_rope_write<FMT_FP4, 0, H>)
+               : (interleaved ? &mx_rope_write<FMT_FP8, 1, H> : &mx_rope_write<FMT_FP8, 0, H>);
+}
 
 int run_rope(const mxg_kv_cache_t *c, const void *q, void *q_out, const void *k, const void *v, int64_t q_heads,
              int64_t q_stride, int64_t q_out_stride, int64_t k_stride, int64_t v_stride, const int64_t *positions,
@@ -29,7 +35,7 @@ int run_rope(const mxg_kv_cache_t *c, const void *q, void *q_out, const void *k,
     const int64_t dim = c->head_dim, width = c->kv_heads * dim, q_width = q_heads * dim;
     if (rot < 16 || rot > dim)
         return MXG_ERR_SHAPE;
-    const int64_t most = std::max(head_groups(q_heads), head_groups(c->kv_heads)) * kRopeHeads * dim;
+    const int64_t most = cdiv(std::max(q_heads, c->kv_heads), kRopeHeads) * kRopeHeads * dim;
     if (tokens > ((int64_t)1 << 30) / (most / 8) || k_stride < width || v_stride < width || k_stride > INT32_MAX ||
         v_stride > INT32_MAX || q_stride < q_width || q_out_stride < q_width || q_stride > INT32_MAX ||
         q_out_stride > INT32_MAX)
@@ -70,8 +76,10 @@ int run_rope(const mxg_kv_cache_t *c, const void *q, void *q_out, const void *k,
     a.npositions = npositions;
     a.rot = (int)rot;
     a.q_heads = (int)q_heads;
-    a.q_groups = (int)head_groups(q_heads);
-    a.kv_groups = (int)head_groups(c->kv_heads);
+    // (pieces and units of one head each: the measured sides are at kRopeHeads)
+    const bool many = tokens * (q_heads * (dim / 16) + 2 * c->kv_heads * (dim / 8)) > 1 << 19;
+    a.q_groups = (int)(many ? cdiv(q_heads, kRopeHeads) : q_heads);
+    a.kv_groups = (int)(many ? cdiv(c->kv_heads, kRopeHeads) : c->kv_heads);
     const int64_t q_token = a.q_groups * (dim / 16), kv_token = a.kv_groups * (dim / 8);
     a.units = (int)(tokens * q_token);
     a.kv.n = (int)(tokens * kv_token);
@@ -81,8 +89,7 @@ int run_rope(const mxg_kv_cache_t *c, const void *q, void *q_out, const void *k,
     a.kv_group = fast_div((unsigned)(dim / 8));
     a.q_blocks = (int)cdiv(a.units, 256);
     a.kv_blocks = (int)cdiv(a.kv.n, 256);
-    void (*fn)(RopeArgs) = c->is_fp4 ? (interleaved ? &mx_rope_write<FMT_FP4, 1> : &mx_rope_write<FMT_FP4, 0>)
-                                     : (interleaved ? &mx_rope_write<FMT_FP8, 1> : &mx_rope_write<FMT_FP8, 0>);
+    const RopeFn fn = many ? rope_fn<kRopeHeads>(c->is_fp4 != 0, interleaved != 0) : rope_fn<1>(c->is_fp4 != 0, interleaved != 0);
     hipLaunchKernelGGL(fn, dim3((unsigned)(a.q_blocks + 2 * a.kv_blocks)), dim3(256), 0, stream, a);
     return host_hip_status(hipGetLastError());
 }
