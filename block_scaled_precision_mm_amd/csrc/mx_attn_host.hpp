@@ -227,7 +227,7 @@ int run_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, 
         return MXG_ERR_PTR_ALIGN;
     const int64_t group = q_heads / cache->kv_heads;
     const AttnPlan plan = TREE ? tree_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new,
-                                           std::min<int64_t>(table_width * cache->page_size, window > 0 ? window + max_new : INT32_MAX))
+                                           std::min<int64_t>(table_width * cache->page_size, window > 0 ? std::min<int64_t>(window, 1 << 30) + max_new : INT32_MAX))
                                : attn_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new);
     for (int i = 0; i < plan.n; ++i)        // (split ones are far below)
         if (plan.base[i] > kMaxThreads / kAttnThreads[plan.which[i]])
