@@ -100,7 +100,7 @@ struct AttnArgs {
     float per_target;                       // KV heads / workgroups that can run at once
     const unsigned long long *mask;         // trees of drafted tokens: [tokens][mask_words], the nodes that each sees
     int mask_words;
-    int resident;                           // (trees) workgroups that can run at once
+    int resident, halves;                   // (trees) workgroups that can run at once; per_target is of twice as many
 };
 
 // One workgroup's work.
@@ -202,14 +202,14 @@ __device__ __forceinline__ int cdiv_u(int a, int b) { return (int)(((unsigned)a 
 // 40 nodes over 131072 and 81000 keys, 272 items of 256 rows for 256
 // workgroups, took 650 us, and in one round 400.)  Where the row tiles alone are
 // too many for that, or it would leave the workgroups half idle: the average
-// work, which cuts none of like sequences, or half of it where some sequence
-// has far more (32 sequences of 100 to 16000 keys 85 us instead of 90).
+// work, which cuts none of like sequences, or (halves: `least` is half of the
+// average) half of it where some sequence has far more (32 sequences of 100 to
+// 16000 keys 85 us instead of 90).
 __device__ __forceinline__ int one_round(const AttnArgs &p, const AttnSeq &q, float total, int least)
 {
-    // (least is half of the average work)
     if (p.seqs > 64)
         return least;
-    const int rounds = __any(q.ktiles > 4 * least) ? least : 2 * least;
+    const int rounds = !p.halves || __any(q.ktiles > 4 * least) ? least : 2 * least;
     const int last = p.seqs > 1 ? 63 : 0;
     int tiles = p.heads * q.rtiles;
     if (p.seqs > 1)

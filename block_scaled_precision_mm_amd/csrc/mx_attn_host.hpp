@@ -174,7 +174,8 @@ AttnPlan tree_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
     // over 16027 keys 40 us instead of 31; with 256, 1 of 200 over
     // 4296 48 instead of 43)
     p.resident = p.which[0] == ROWS_256 ? 256 : 512;
-    p.target[0] = 2 * p.resident;
+    // (tiles of many rows: their parts' joins cost more than halves gain)
+    p.target[0] = p.which[0] <= ROWS_32 ? 2 * p.resident : p.resident;
     p.bytes[0] = p.base[0] <= kTreeTiles ? (size_t)2 * p.target[0] * attn_slot_bytes(bm, (int)dim) : 0;
     return p;
 }
@@ -273,6 +274,7 @@ int run_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, 
         a.rows_upto = plan.upto[i];
         a.per_target = (float)a.heads / (float)plan.target[i];
         a.resident = plan.resident;
+        a.halves = plan.target[i] > plan.resident;
         const int64_t grid = plan.base[i] + (parts ? plan.target[i] : 0);
         hipLaunchKernelGGL(attn_fn<TREE>(which, cache->is_fp4 != 0, cache->head_dim, cache->page_size), dim3((unsigned)grid),
                            dim3(kAttnThreads[which]), 0, (hipStream_t)stream, a);

@@ -501,7 +501,8 @@ size_t mx_paged_attention_workspace_bytes(const mxg_kv_cache_t *cache, int64_t s
  * q, q_out    BF16, token t at element t * q_stride / t * q_out_stride, its
  *             [q_heads][head_dim] values contiguous, 16-byte aligned.  q_out is
  *             q itself (with the same stride: rotated in place) or lies apart
- *             from it.  q_heads 0: no queries, both may be NULL.
+ *             from it, and apart from k and v.  q_heads 0: no queries, both may
+ *             be NULL.
  * k, v        as for mx_kv_cache_write; k is not written.
  * slots       as for mx_kv_cache_write.
  * positions   DEVICE memory, int64 [tokens], 8-byte aligned.  One outside
@@ -580,6 +581,7 @@ size_t mx_tree_attention_workspace_bytes(const mxg_kv_cache_t *cache, int64_t se
  * offs        output, int32 [groups]: the end row of each expert, as
  *             mx_grouped_mm_* take it.
  * pos         output, int32 [tokens][top_k]: the row of each assignment, or -1.
+ *             (outputs overlap no input)
  * workspace   mx_moe_dispatch_workspace_bytes bytes where that is not 0
  *             (above 4096 assignments), 16-byte aligned, its first 64 KiB zero
  *             when it is allocated and left zero by every call: one workspace
