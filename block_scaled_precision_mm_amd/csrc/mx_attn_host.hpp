@@ -156,6 +156,11 @@ AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
 //     32 of 32 over 4096                        181   118   112   128
 //     1 of 200 over 16200                       165   108    87    84
 //     32 of 64 over 4096                        344   230   171   152
+//     16 of 64 over 300                          36    30    27    31
+//     16 of 64 over 1000                         63    46    53    56
+//     32 of 64 over 100                          54    49    28    30
+//     32 of 64 over 1000                        119    89    60    57
+//     8 of 200 over 300                          67    61    44    39
 AttnPlan tree_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, int64_t dim, int64_t max_new, int64_t keys)
 {
     AttnPlan p = {};
@@ -163,7 +168,7 @@ AttnPlan tree_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
     const int64_t rows = tokens * group, mean = cdiv(rows, std::max<int64_t>(some, 1)), tiles = heads * cdiv(rows, 32);
     p.n = 1;
     p.which[0] = max_new * group <= 16 || (tiles * keys < 400000 && heads * cdiv(rows, 16) <= 512) ? ROWS_16
-                 : mean <= 64 || tiles * keys < 2500000                                           ? ROWS_32
+                 : mean <= 64 || (tiles < 1400 && tiles * keys < 2500000)                         ? ROWS_32
                  : mean <= 128                                                                    ? ROWS_128
                                                                                                   : ROWS_256;
     const int bm = kAttnBM[p.which[0]];
