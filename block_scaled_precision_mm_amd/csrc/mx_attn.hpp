@@ -100,7 +100,7 @@ struct AttnArgs {
     float per_target;                       // KV heads / workgroups that can run at once
     const unsigned long long *mask;         // trees of drafted tokens: [tokens][mask_words], the nodes that each sees
     int mask_words;
-    int resident, halves;                   // (trees) workgroups that can run at once; per_target is of twice as many
+    int resident;                           // (trees) workgroups that can run at once
 };
 
 // One workgroup's work.
@@ -202,14 +202,15 @@ __device__ __forceinline__ int cdiv_u(int a, int b) { return (int)(((unsigned)a 
 // 40 nodes over 131072 and 81000 keys, 272 items of 256 rows for 256
 // workgroups, took 650 us, and in one round 400.)  Where the row tiles alone are
 // too many for that, or it would leave the workgroups half idle: the average
-// work, which cuts none of like sequences, or (halves: `least` is half of the
-// average) half of it where some sequence has far more (32 sequences of 100 to
-// 16000 keys 85 us instead of 90).
+// work, which cuts none of like sequences, or 1.3 times that where some sequence
+// has far more: there the long ones' items go first (plan_item), so that short
+// ones fill the end (32 sequences of 100 to 16000 keys 77 us; with the average
+// work 89, twice that 83, half of it in the sequences' order 92).
 __device__ __forceinline__ int one_round(const AttnArgs &p, const AttnSeq &q, float total, int least)
 {
     if (p.seqs > 64)
         return least;
-    const int rounds = !p.halves || __any(q.ktiles > 4 * least) ? least : 2 * least;
+    const int rounds = __any(q.ktiles > 2 * least) ? (int)(1.3f * (float)least) : least;
     const int last = p.seqs > 1 ? 63 : 0;
     int tiles = p.heads * q.rtiles;
     if (p.seqs > 1)
@@ -282,6 +283,19 @@ __device__ __forceinline__ bool plan_item(const AttnArgs &p, int item, int min_t
                 tiles_upto = wave_prefix(tiles_upto);
             }
         }
+        int owned = mine;
+        if (TREE && !JOIN && p.seqs > 1 && p.seqs <= 64) {
+            // the items of sequences of long parts first
+            const bool is_long = 2 * q.ktiles >= chunk;
+            owned = is_long ? mine : 0;
+            upto = wave_prefix(owned);
+            const int longs = lane_value(upto, 63);
+            if (item >= longs) {
+                item -= longs;
+                owned = is_long ? 0 : mine;
+                upto = wave_prefix(owned);
+            }
+        }
         const int all = lane_value(upto, p.seqs > 1 ? 63 : 0);
         if (item >= all) {
             item -= all;
@@ -296,7 +310,7 @@ __device__ __forceinline__ bool plan_item(const AttnArgs &p, int item, int min_t
         it.tok0 = lane_value(q.tok0, at);
         it.ntok = lane_value(q.ntok, at);
         it.len = lane_value(q.len, at);
-        const int rtiles = lane_value(q.rtiles, at), sparts = lane_value(parts, at), smine = lane_value(mine, at);
+        const int rtiles = lane_value(q.rtiles, at), sparts = lane_value(parts, at), smine = lane_value(owned, at);
         item -= lane_value(upto, at) - smine;
         slots += lane_value(slots_upto, at) - (sparts > 1 ? lane_value(myparts, at) : 0);
         tiles += lane_value(tiles_upto, at) - p.heads * rtiles;

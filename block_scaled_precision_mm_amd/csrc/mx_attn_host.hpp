@@ -151,7 +151,7 @@ AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
 //     1 of 16 over 4112                        16.5  23.5    27    29
 //     32 of 16 over 256                        18.5  15.0    18    22
 //     1 of 64 over 16064                         51    40    54    56
-//     32 of 16 over 100 to 16000                112    85    90   151
+//     32 of 16 over 100 to 16000                112    77    90   151
 //     8 of 64 over 4096                          92    57    62    65
 //     32 of 32 over 4096                        181   118   112   128
 //     1 of 200 over 16200                       165   108    87    84
@@ -174,13 +174,11 @@ AttnPlan tree_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
     const int bm = kAttnBM[p.which[0]];
     p.upto[0] = INT32_MAX;
     p.base[0] = heads * (rows / bm + some);
-    // (one_round: items that run at once, or twice as many.  With 768 instead of
-    // 512 the parts' joins cost more than the parts gain: 1 sequence of 27 nodes
-    // over 16027 keys 40 us instead of 31; with 256, 1 of 200 over
-    // 4296 48 instead of 43)
+    // (with 768 instead of 512 the parts' joins cost more than the parts gain:
+    // 1 sequence of 27 nodes over 16027 keys 40 us instead of 31; with 256, 1 of
+    // 200 over 4296 48 instead of 43)
     p.resident = p.which[0] == ROWS_256 ? 256 : 512;
-    // (tiles of many rows: their parts' joins cost more than halves gain)
-    p.target[0] = p.which[0] <= ROWS_32 ? 2 * p.resident : p.resident;
+    p.target[0] = p.resident;
     p.bytes[0] = p.base[0] <= kTreeTiles ? (size_t)2 * p.target[0] * attn_slot_bytes(bm, (int)dim) : 0;
     return p;
 }
@@ -279,7 +277,6 @@ int run_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, 
         a.rows_upto = plan.upto[i];
         a.per_target = (float)a.heads / (float)plan.target[i];
         a.resident = plan.resident;
-        a.halves = plan.target[i] > plan.resident;
         const int64_t grid = plan.base[i] + (parts ? plan.target[i] : 0);
         hipLaunchKernelGGL(attn_fn<TREE>(which, cache->is_fp4 != 0, cache->head_dim, cache->page_size), dim3((unsigned)grid),
                            dim3(kAttnThreads[which]), 0, (hipStream_t)stream, a);
