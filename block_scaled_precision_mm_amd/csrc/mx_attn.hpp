@@ -896,22 +896,22 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
 constexpr int kTileParts = 8;
 
 // The join of row tiles of many rows, a kernel of its own behind mx_attn_tile:
-// 512 runs of a row tile per workgroup.  (The last workgroup of a row tile,
-// joining alone as above, took 30 us for 31 parts of 64 rows.)
-constexpr int attn_join_blocks(int rows, int dim) { return cdiv_c(rows * dim / 8, 512); }
+// 512 runs of a row tile per workgroup, 256 of trees.  (The last workgroup of a
+// row tile, joining alone as above, took 30 us for 31 parts of 64 rows.)
+constexpr int attn_join_blocks(int rows, int dim, int tree) { return cdiv_c(rows * dim / 8, tree ? 256 : 512); }
 
 template <int D, int BM, int TREE>
 __global__ __launch_bounds__(256)
 void mx_attn_join(AttnArgs p)
 {
-    constexpr int RUNS = D / 8, SUB = attn_join_blocks(BM, D);
+    constexpr int RUNS = D / 8, SUB = attn_join_blocks(BM, D, TREE), EACH = TREE ? 1 : 2;
     AttnItem it;
     if (!plan_item<TREE, BM, 64, 1>(p, blockIdx.x / SUB, kTileParts, it) || it.parts == 1)
         return;
     const int n = min(BM, it.ntok * p.group - it.row0) * RUNS;
 #pragma unroll 1
-    for (int u = 0; u < 2; ++u) {
-        const int i = (blockIdx.x % SUB * 2 + u) * 256 + threadIdx.x;
+    for (int u = 0; u < EACH; ++u) {
+        const int i = (blockIdx.x % SUB * EACH + u) * 256 + threadIdx.x;
         if (i < n) {
             AttnSums s;
             attn_sum_parts<D, BM>(p, it, i, 0, 1, it.parts, s);

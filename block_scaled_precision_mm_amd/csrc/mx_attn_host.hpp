@@ -284,7 +284,7 @@ int run_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, 
         if (rc)
             return rc;
         if (parts && which >= ROWS_128) {
-            const int64_t join = std::min<int64_t>(plan.base[i], plan.target[i]) * attn_join_blocks(kAttnBM[which], (int)cache->head_dim);
+            const int64_t join = std::min<int64_t>(plan.base[i], plan.target[i]) * attn_join_blocks(kAttnBM[which], (int)cache->head_dim, TREE);
             hipLaunchKernelGGL(attn_join_fn<TREE>(which, cache->head_dim), dim3((unsigned)join), dim3(256), 0,
                                (hipStream_t)stream, a);
             rc = host_hip_status(hipGetLastError());
