@@ -334,3 +334,34 @@ def test_there_and_back_on_another_stream_and_replayed():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, held))
+
+
+def test_offsets_past_32_bits():
+    """Rows of more than 2^32 codes and 2^33 bytes: dispatched, combined, and their gradient, at rows throughout."""
+    tokens, top_k, K, E = 560000, 8, 1024, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((tokens, K), generator=g, device="cuda", dtype=torch.bfloat16)
+    ids = torch.randint(0, E, (tokens, top_k), generator=g, device="cuda")
+    y, ys, offs, pos = mx.moe_dispatch(x, ids, E)
+    assert y.numel() > 1 << 32 and int(offs[-1]) == tokens * top_k
+    codes, scales = torch.empty((tokens, K), dtype=torch.uint8, device="cuda"), torch.empty((tokens, K // 32), dtype=torch.uint8, device="cuda")
+    mx.mx_quantize_bf16(x, codes, scales, tokens, K, False)
+    for j in (0, 7):
+        at = pos[:, j].long()
+        assert int(at.max()) * K > 1 << 32
+        for part in range(0, tokens, 70000):
+            rows = at[part:part + 70000]
+            assert torch.equal(y[rows], codes[part:part + 70000]) and torch.equal(ys[rows], scales[part:part + 70000])
+    del y, ys, codes, scales
+    rows, _, _, pos2 = mx.moe_dispatch(x, ids, E, torch.bfloat16)
+    assert torch.equal(pos, pos2)
+    # powers of two: every product and sum of eight like values is exact
+    w = torch.full((tokens, top_k), 0.125, device="cuda")
+    out = mx.moe_combine(rows, pos, w)
+    assert torch.equal(out, x)
+    d_y, d_w = mx.moe_combine_grad(x, rows, pos, w)
+    torch.cuda.synchronize()
+    assert torch.equal(d_w, d_w[:, :1].expand(-1, top_k))
+    for part in range(0, tokens, 70000):
+        at = pos[part:part + 70000, 3].long()
+        assert torch.equal(d_y[at], x[part:part + 70000] * 0.125)

@@ -211,3 +211,21 @@ def test_other_stream_and_replays():
         torch.cuda.synchronize()
         assert same(out, q)
         assert all(torch.equal(a.cpu(), b) for a, b in zip(c.parts(), parts))
+
+
+# (past 2^19 pieces a thread has four heads)
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("fmt,inter,rot", [("fp8", False, 128), ("fp8", True, 128), ("fp4", False, 48), ("fp4", True, 16)])
+@pytest.mark.parametrize("tokens,q_heads,heads", [(1100, 32, 8), (1777, 33, 3), (2500, 9, 9)])
+def test_many_tokens(tokens, q_heads, heads, fmt, inter, rot, in_place):
+    assert tokens * (q_heads * 8 + 2 * heads * 16) > 1 << 19
+    Case(tokens, q_heads, heads, rot=rot, inter=inter, fmt=fmt, pad=8).check("many tokens", in_place=in_place)
+
+
+def test_many_keys_alone():
+    c = Case(9000, 1, 2)
+    assert 9000 * 2 * 2 * 16 > 1 << 19
+    _, parts = c.want()
+    mx.mx_rope_cache_write(c.cache, None, c.k, c.v, c.positions, c.slots, c.table)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.cpu(), b) for a, b in zip(c.parts(), parts))

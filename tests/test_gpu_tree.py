@@ -111,7 +111,7 @@ def test_many_nodes(fmt, dim, nodes):
 @pytest.mark.parametrize("group,nodes", [(1, 300), (4, 140), (8, 70), (16, 40)])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_tiles_of_many_rows(group, nodes, dim):
-    """Several sequences of many rows: the kernel of many rows, in both tile sizes."""
+    """Several sequences of many rows."""
     Case([(nodes, nodes + 90), (nodes, nodes + 700), (nodes, nodes), (nodes, nodes + 33)], dim=dim, heads=1, group=group).check("tiles")
 
 
@@ -160,7 +160,7 @@ def test_masks_that_are_no_trees():
         assert (out[empty] == 0).all() and (lse[empty] == -np.inf).all()
 
 
-def test_rows_that_see_nothing_in_the_kernel_of_many_rows():
+def test_many_rows_that_see_nothing():
     n = 150
     sees = [np.zeros((n, n), bool) for _ in range(4)]
     sees[1][10, 3] = True
@@ -186,7 +186,7 @@ def test_more_sequences_than_lanes():
     Case(seqs, heads=1, group=2).check("131 sequences", max_new=6)
 
 
-def test_both_kernels_in_a_call():
+def test_few_and_many_nodes_in_a_call():
     Case([(1, 50), (150, 400), (3, 900), (90, 100)], heads=2, group=4).check("mixed")
 
 
