@@ -167,9 +167,13 @@ AttnPlan tree_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
     const int64_t some = std::min(seqs, tokens);        // sequences with a node
     const int64_t rows = tokens * group, mean = cdiv(rows, std::max<int64_t>(some, 1)), tiles = heads * cdiv(rows, 32);
     p.n = 1;
+    // (256 rows in as many rounds of 256 items, 128 in as many of 512, 1.17 times
+    // as long: 9 sequences of 880 rows over 500 keys, 288 items of 256 rows or 504
+    // of 128, 48 and 35 us)
+    const int64_t rounds256 = cdiv(heads * some * cdiv(mean, 256), 256), rounds128 = cdiv(heads * some * cdiv(mean, 128), 512);
     p.which[0] = max_new * group <= 16 || (tiles * keys < 400000 && heads * cdiv(rows, 16) <= 512) ? ROWS_16
                  : mean <= 64 || (tiles < 1400 && tiles * keys < 2500000)                         ? ROWS_32
-                 : mean <= 128                                                                    ? ROWS_128
+                 : mean <= 128 || 117 * rounds128 < 100 * rounds256                               ? ROWS_128
                                                                                                   : ROWS_256;
     const int bm = kAttnBM[p.which[0]];
     p.upto[0] = INT32_MAX;
