@@ -44,6 +44,18 @@
 // last (few rows) or by a second kernel (many rows), in a fixed order, so
 // results do not depend on timing.
 //
+// Trees of drafted tokens (TREE).  The rows of a sequence see its whole context
+// and of the new keys, its nodes, those of their mask's bits.  So only tiles
+// that hold a node, the last of a sequence, look at masks: a word or two per
+// row and tile, in the branch that other partly seen tiles take; the rest is
+// the same loop.  Bound as it: one tree of 27 nodes over 1051 keys 12.6 us (the
+// chain of dependent loads and the join of the parts), 32 of 16 over 100 to
+// 16000 keys, 64 rows a KV head, 75 us (239 MB, 3.2 TB/s; every key expanded
+// for two row tiles, VALU and MFMA issue), two of 488 and 320 rows over 131072
+// and 81000 keys in E2M1 384 to 404 us (0.95 PFLOP/s).  A tree's launch has one
+// kernel for all rows; its parts are chosen so that items run at once
+// (one_round), as there are too few rows for many rounds.
+//
 // Masked places.  Scores of unseen keys are replaced, never added to;
 // values of slots past the sequence's end or on pages outside the cache are
 // replaced by zeros as they are expanded.  A NaN or infinity (a code under a
