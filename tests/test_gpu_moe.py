@@ -365,3 +365,9 @@ def test_offsets_past_32_bits():
     for part in range(0, tokens, 70000):
         at = pos[part:part + 70000, 3].long()
         assert torch.equal(d_y[at], x[part:part + 70000] * 0.125)
+
+
+@pytest.mark.parametrize("tokens", [8191, 8192, 8193, 8320])
+def test_dispatch_at_the_most_chunks_that_are_added_up_by_each_workgroup(tokens):
+    check_dispatch(tokens, 8, 40, 32)
+    check_dispatch(tokens * 8, 1, 1024, 32, "bf16")
