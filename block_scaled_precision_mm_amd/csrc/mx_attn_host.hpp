@@ -187,6 +187,13 @@ AttnPlan tree_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
     return p;
 }
 
+// The most keys that a row of a tree may see, for tree_plan: what the table has
+// room for, and with a window that many and the nodes.
+int64_t tree_keys(int64_t table_width, int64_t page_size, int64_t window, int64_t max_new)
+{
+    return std::min(table_width * page_size, window > 0 ? std::min<int64_t>(window, 1 << 30) + max_new : (int64_t)INT32_MAX);
+}
+
 bool attn_shape_ok(const mxg_kv_cache_t *c, int64_t seqs, int64_t tokens, int64_t q_heads, int64_t max_new)
 {
     return seqs >= 0 && seqs <= 65536 && tokens >= 0 && q_heads >= c->kv_heads && q_heads <= 65536 &&
@@ -235,7 +242,7 @@ int run_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, 
         return MXG_ERR_PTR_ALIGN;
     const int64_t group = q_heads / cache->kv_heads;
     const AttnPlan plan = TREE ? tree_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new,
-                                           std::min<int64_t>(table_width * cache->page_size, window > 0 ? std::min<int64_t>(window, 1 << 30) + max_new : INT32_MAX))
+                                           tree_keys(table_width, cache->page_size, window, max_new))
                                : attn_plan(seqs, tokens, cache->kv_heads, group, cache->head_dim, max_new);
     for (int i = 0; i < plan.n; ++i)        // (split ones are far below)
         if (plan.base[i] > kMaxThreads / kAttnThreads[plan.which[i]])
