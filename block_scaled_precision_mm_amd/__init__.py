@@ -833,7 +833,8 @@ def mx_tree_attention(cache, q, ends, lens, table, mask, out, lse=None, scale=No
     mx_tree_attention): mask int64 [tokens][words], bit j % 64 of word j / 64
     of a token's row set where it sees the j-th new token of its sequence,
     itself included (tree_mask makes it from parents); all else as for
-    mx_paged_attention."""
+    mx_paged_attention, but that FP16 and FP32 outputs take the weights in two
+    BF16 parts."""
     dev, seqs, tokens, heads, dim, qs, kind = _attention_args(cache, q, ends, lens, table, out, lse)
     if mask is None or mask.dtype is not _I64T or mask.get_device() != dev or mask.dim() != 2 or mask.shape[0] != tokens or \
             not mask.is_contiguous():

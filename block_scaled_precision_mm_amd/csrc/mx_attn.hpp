@@ -14,8 +14,16 @@
 // significant bits), both products run on the BF16 MFMA with FP32
 // accumulation, q.k of the given BF16 q is exact but for the accumulation, x,
 // m and the sums are FP32.  p is rounded to BF16 as the second product's
-// operand (half a step: 2^-8 of each p); the sum of the p's takes them
-// unrounded.
+// operand (half a step: 2^-8 of each p): values need BF16's range (FP16 would
+// lose a block whose scale is far from the others'), and a BF16 output is
+// rounded as coarsely itself: relative to 64 bits it is off by 0.0020, where its
+// own rounding makes 0.0017, in the mean over a call's outputs.  The FP16 and
+// FP32 outputs of trees (P2) take p in two parts, BF16(p) and BF16 of the rest,
+// with a second MFMA each: 2^-16 of each p, and FP32 outputs off by 2e-6 instead
+// of 0.0012.  It costs nothing where loads and joins bound a call, and a third
+// where the MFMAs do (us, BF16 and FP32 outputs: 27 nodes over 1051 keys 12.7
+// and 12.8, 32 ragged trees 75 and 80, 24 under a window 24.1 and 26.4, two over
+// 131072 and 80868 keys 400 and 538).  The sum of the p's takes them unrounded.
 //
 // The rows of one KV head.  All G = q_heads / kv_heads query heads of a KV
 // head read the same keys, so a tile's rows are (token, head of the group)
@@ -961,7 +969,7 @@ void mx_attn_join(AttnArgs p)
 //
 // PAGED: pages of 16 keys or more, so that the two pages of a tile are
 // scalars and the lanes' offsets the same for every tile.
-template <int F, int D, int QT, int PAGED, int TREE>
+template <int F, int D, int QT, int PAGED, int TREE, int P2>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(QT > 1 ? 2 : F == FMT_FP8 && D == 128 ? 3 : 4)))
 void mx_attn_rows(AttnArgs p)
 {
@@ -1118,7 +1126,7 @@ void mx_attn_rows(AttnArgs p)
         // the loop would wait for the loads it has just issued, to merge them
         // with the registers' old contents)
         load(key + BN);
-        bf16x8v pb[QT];
+        bf16x8v pb[QT], rest[P2 ? QT : 1];
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             if (!whole) {
@@ -1134,6 +1142,8 @@ void mx_attn_rows(AttnArgs p)
                     const float w = __builtin_amdgcn_exp2f(fmaf(x[t][e >> 2][e & 3], p.c, -ref));
                     sum += w;
                     pb[t][e] = (__bf16)w;
+                    if constexpr (P2)
+                        rest[t][e] = (__bf16)(w - (float)pb[t][e]);
                 }
                 return sum;
             };
@@ -1169,8 +1179,11 @@ void mx_attn_rows(AttnArgs p)
             const u2v a = lds_read_tr(vread + 32 * d), b = lds_read_tr(vread + 16 * VROW + 32 * d);
             const bf16x8v f = as_bf16x8(u4v{a.x, a.y, b.x, b.y});
 #pragma unroll
-            for (int t = 0; t < QT; ++t)
+            for (int t = 0; t < QT; ++t) {
                 o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, pb[t], o[t][d], 0, 0, 0);
+                if constexpr (P2)
+                    o[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, rest[t], o[t][d], 0, 0, 0);
+            }
         }
         wave_fence();
     }
@@ -1319,7 +1332,7 @@ __device__ __forceinline__ TileRange tiles_touching(int key0, int lo, int hi)
     return {a, lo < hi ? max(b - a, 0) : 0};
 }
 
-template <int F, int D, int NW, int PAGED, int TREE>
+template <int F, int D, int NW, int PAGED, int TREE, int P2>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void mx_attn_tile(AttnArgs p)
 {
@@ -1384,10 +1397,16 @@ void mx_attn_tile(AttnArgs p)
             o[d][i] = 0.0f;
     // (0 for rows that are not there, whose scores are 0)
     float m = row.token >= 0 ? -__builtin_inff() : 0.0f, l = 0.0f;
-    bf16x8v pb[4];
+    bf16x8v pb[4], rest[P2 ? 4 : 1];
+    auto clear_weights = [&] {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
+        for (int i = 0; i < 4; ++i) {
+            pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
+            if constexpr (P2)
+                rest[i] = pb[i];
+        }
+    };
+    clear_weights();
 
     // the loaded tile: this thread's chunks, and the keys that are there
     u4v codes[NI];
@@ -1548,6 +1567,8 @@ void mx_attn_tile(AttnArgs p)
             const bf16x8v f = as_bf16x8(frag[b % 3][i]);
             if constexpr (b < 4) {
                 o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, pb[b], o[i], 0, 0, 0);
+                if constexpr (P2)
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, rest[b], o[i], 0, 0, 0);
             } else {
                 constexpr int s = (b - 4) * (DT / 2) + (i >> 1);
                 if constexpr (s == 0)
@@ -1608,6 +1629,8 @@ void mx_attn_tile(AttnArgs p)
                 const float w = __builtin_amdgcn_exp2f(fmaf(x[e >> 4][e & 15], p.c, -ref));
                 sum += w;
                 pb[e >> 3][e & 7] = (__bf16)w;
+                if constexpr (P2)
+                    rest[e >> 3][e & 7] = (__bf16)(w - (float)pb[e >> 3][e & 7]);
             }
             return sum;
         };
@@ -1644,9 +1667,7 @@ void mx_attn_tile(AttnArgs p)
         } else {
             // (p of a tile that no row of the wave sees; and said for x as well,
             // so that nothing keeps its registers through the other phase)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
+            clear_weights();
         }
         // (loads past the last tile are of page 0 of the cache and not used.
         // Under a condition the loop would wait for the loads it has just

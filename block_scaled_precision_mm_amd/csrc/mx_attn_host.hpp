@@ -43,32 +43,32 @@ AttnFn attn_join_fn(int which, int64_t dim)
     return dim == 64 ? &mx_attn_join<64, 256, TREE> : &mx_attn_join<128, 256, TREE>;
 }
 
-template <int F, int D, int PAGED, int TREE>
+template <int F, int D, int PAGED, int TREE, int P2>
 AttnFn attn_fn(int which)
 {
     switch (which) {
-    case ROWS_16: return &mx_attn_rows<F, D, 1, PAGED, TREE>;
-    case ROWS_32: return &mx_attn_rows<F, D, 2, PAGED, TREE>;
-    case ROWS_128: return &mx_attn_tile<F, D, 4, PAGED, TREE>;
-    default: return &mx_attn_tile<F, D, 8, PAGED, TREE>;
+    case ROWS_16: return &mx_attn_rows<F, D, 1, PAGED, TREE, P2>;
+    case ROWS_32: return &mx_attn_rows<F, D, 2, PAGED, TREE, P2>;
+    case ROWS_128: return &mx_attn_tile<F, D, 4, PAGED, TREE, P2>;
+    default: return &mx_attn_tile<F, D, 8, PAGED, TREE, P2>;
     }
 }
 
-template <int F, int D, int TREE>
+template <int F, int D, int TREE, int P2>
 AttnFn attn_fn(int which, int64_t page_size)
 {
     // mx_attn_rows takes tiles of two pages, mx_attn_tile loads of one wave
     // (64 chunks of 16 bytes)
     const bool paged = page_size >= (which <= ROWS_32 ? 16 : 64 / AttnGeom<F, D>::CH);
-    return paged ? attn_fn<F, D, 1, TREE>(which) : attn_fn<F, D, 0, TREE>(which);
+    return paged ? attn_fn<F, D, 1, TREE, P2>(which) : attn_fn<F, D, 0, TREE, P2>(which);
 }
 
-template <int TREE>
+template <int TREE, int P2>
 AttnFn attn_fn(int which, bool fp4, int64_t dim, int64_t page_size)
 {
     if (dim == 64)
-        return fp4 ? attn_fn<FMT_FP4, 64, TREE>(which, page_size) : attn_fn<FMT_FP8, 64, TREE>(which, page_size);
-    return fp4 ? attn_fn<FMT_FP4, 128, TREE>(which, page_size) : attn_fn<FMT_FP8, 128, TREE>(which, page_size);
+        return fp4 ? attn_fn<FMT_FP4, 64, TREE, P2>(which, page_size) : attn_fn<FMT_FP8, 64, TREE, P2>(which, page_size);
+    return fp4 ? attn_fn<FMT_FP4, 128, TREE, P2>(which, page_size) : attn_fn<FMT_FP8, 128, TREE, P2>(which, page_size);
 }
 
 // Most rows (new tokens x heads of a group) of a sequence for mx_attn_rows,
@@ -289,8 +289,12 @@ int run_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, 
         a.per_target = (float)a.heads / (float)plan.target[i];
         a.resident = plan.resident;
         const int64_t grid = plan.base[i] + (parts ? plan.target[i] : 0);
-        hipLaunchKernelGGL(attn_fn<TREE>(which, cache->is_fp4 != 0, cache->head_dim, cache->page_size), dim3((unsigned)grid),
-                           dim3(kAttnThreads[which]), 0, (hipStream_t)stream, a);
+        // (weights in two parts where the output has more bits than BF16)
+        AttnFn fn = attn_fn<TREE, 0>(which, cache->is_fp4 != 0, cache->head_dim, cache->page_size);
+        if constexpr (TREE)
+            if (out_dtype != MXG_OUT_BF16)
+                fn = attn_fn<TREE, 1>(which, cache->is_fp4 != 0, cache->head_dim, cache->page_size);
+        hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(kAttnThreads[which]), 0, (hipStream_t)stream, a);
         rc = host_hip_status(hipGetLastError());
         if (rc)
             return rc;

@@ -31,9 +31,13 @@ def width(case, page):
 
 def plans():
     """(rows per tile, sequences, page size, columns, window, max_new) of every call."""
-    for cases, windows in ((WINDOWED, WINDOWS), (LONG, LONG_WINDOWS), (MANY, (0,))):
+    for cases, windows in ((WINDOWED, WINDOWS), (LONG, LONG_WINDOWS), (MANY, (0,)), (SHORT, (0, 5))):
         for rows, case in cases.items():
             for page in (2, 16):
                 for window in windows:
                     most = max(n for n, _ in case[0]) if case[2] is None else case[2]
                     yield rows, case[0], page, width(case, page), window, most
+
+# rows that see few keys, none or a few of a context
+SHORT = {16: ([(40, 43), (90, 90), (33, 60)], 0, None), 32: ([(40, 43), (90, 90), (33, 60)], 40000, 40000),
+         128: ([(20, 23), (31, 31), (25, 40)], 1 << 20, 1 << 22), 256: ([(40, 43), (90, 90), (33, 60)], 1 << 20, 1 << 22)}
