@@ -860,7 +860,8 @@ def tree_attention(cache, q, ends, lens, table, mask, out_dtype=torch.bfloat16, 
 def tree_mask(parents, words=None) -> torch.Tensor:
     """The mask rows of one sequence's tree: parents a list, for each node the
     earlier node that it continues, or -1 for one that continues the context.
-    int64 [nodes][words] on the CPU."""
+    int64 [nodes][words] on the CPU.  All ancestors are in it: a window hides
+    none of them by itself."""
     rows = []
     for i, parent in enumerate(parents):
         if not -1 <= parent < i:

@@ -535,7 +535,11 @@ int mx_rope_cache_write(const mxg_kv_cache_t *cache, const void *q, void *q_out,
  *   node j      where bit j % 64 of word j / 64 of its mask is set (itself too)
  *   context     key j < L - n; with a window > 0 also j > L - n + d - window,
  *               d the number of nodes that it sees less one, but at least 0:
- *               its depth.  Nodes are seen whatever the window.
+ *               its depth.  Nodes are seen whatever the window, also those
+ *               that are window places or more above: where a tree is deeper
+ *               than a window that is to hide them, the caller leaves their
+ *               bits out.  (Node and window - 1 ancestors left, the rule above
+ *               gives no context, as a window of positions does.)
  *
  * mask        DEVICE memory, 64-bit words [tokens][mask_words], 8-byte aligned:
  *             row t that of row t of q.  Bits of nodes that the sequence does
