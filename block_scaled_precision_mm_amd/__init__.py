@@ -1043,7 +1043,8 @@ def mx_moe_combine_grad(d_out, y, pos, weights, d_y, d_y_scale=None, d_weights=N
     """The gradients of mx_moe_combine (C ABI mx_moe_combine_grad): d_out
     [tokens][N] and y [rows][N] of one type; d_y [rows][N] of that type, or
     1-byte E4M3 codes or E2M1 pairs with d_y_scale [rows][N / 32]; d_weights
-    float32 [tokens][top_k] or None (then y may be None)."""
+    float32 [tokens][top_k] or None (then y may be None).  The rows that pos
+    names are distinct."""
     dev = _here()
     tokens, top_k, pw = _combine_args(pos, weights, dev)
     dtype = _float_kind("d_out", d_out)

@@ -617,7 +617,7 @@ size_t mx_moe_dispatch_workspace_bytes(int64_t tokens, int64_t top_k, int64_t gr
  * pos         DEVICE int32 [tokens][top_k], any content.
  * weights     DEVICE FP32 [tokens][top_k], or NULL for ones.
  * out         [tokens][N] of out_dtype (BF16, FP16, FP32), 16-byte aligned;
- *             every value is written.
+ *             every value is written.  It overlaps no input.
  * tokens, top_k  as for mx_moe_dispatch.  N a multiple of 8, at most 2^20,
  *             tokens * N below 2^34; rows 0 .. 2^31 - 1.
  *
@@ -638,9 +638,12 @@ int mx_moe_combine(const void *y, int y_dtype, const int32_t *pos, const float *
  *             to BF16 and quantized as mx_quantize_bf16 does, codes into d_y and
  *             scales into d_y_scale [rows][N/32]: the A operand of the backward
  *             products (N a multiple of 32).  Rows that no assignment has are not
- *             written; the rows of pos that lie in [0, rows) are distinct (of
- *             two assignments with one row either's gradient may be left there).
+ *             written.  The rows of pos that lie in [0, rows) are distinct: a row
+ *             that two assignments have holds parts of both their gradients
+ *             afterwards, codes and scales too, in no order, and not their sum
+ *             (d_weights and the other rows are right all the same).
  * d_weights   FP32 [tokens][top_k], or NULL: not computed, and y not read.
+ *             (the outputs overlap no input)
  *
  * All else as for mx_moe_combine.
  */
