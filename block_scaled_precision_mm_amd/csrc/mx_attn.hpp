@@ -16,11 +16,11 @@
 // m and the sums are FP32.  p is rounded to BF16 as the second product's
 // operand (half a step: 2^-8 of each p): values need BF16's range (FP16 would
 // lose a block whose scale is far from the others'), and a BF16 output is
-// rounded as coarsely itself: relative to 64 bits it is off by 0.0020, where its
-// own rounding makes 0.0017, in the mean over a call's outputs.  The FP16 and
+// rounded as coarsely itself: relative to 64 bits it is off by 0.0020 to 0.0023,
+// where its own rounding makes 0.0017 (2-norms over a call's outputs).  The FP16 and
 // FP32 outputs of trees (P2) take p in two parts, BF16(p) and BF16 of the rest,
 // with a second MFMA each: 2^-16 of each p, and FP32 outputs off by 2e-6 instead
-// of 0.0012.  It costs nothing where loads and joins bound a call, and a third
+// of 0.0011 to 0.0016.  It costs nothing where loads and joins bound a call, and a third
 // where the MFMAs do (us, BF16 and FP32 outputs: 27 nodes over 1051 keys 12.7
 // and 12.8, 32 ragged trees 75 and 80, 24 under a window 24.1 and 26.4, two over
 // 131072 and 80868 keys 400 and 538).  The sum of the p's takes them unrounded.
