@@ -85,9 +85,19 @@ __device__ __forceinline__ int moe_scan(int *count, int n, int *sums)
 
 // Many assignments, first kernel: each workgroup counts a chunk's; and with many
 // chunks (summed) the one that arrives last turns the counts into the rows
-// before each chunk's.  With few, the second kernel's workgroups add them up
-// themselves, which is one round of loads for each but no chain of them at the
-// end of this kernel (1024 tokens with 8 choices 13.7 us with it, 10.4 without).
+// before each chunk's.  With few, up to kMoeChunks, the second kernel's
+// workgroups add them up themselves, which is a round of loads for each but no
+// chain of them in one workgroup while the GPU waits.  us on the GPU, 8 choices
+// of each token, rows of 1024 into E4M3, added up by each / by the last:
+//     chunks               64          128          256          512
+//        8 experts    24.5  26.2   46.9  44.1   98.0  89.3   210  167
+//       64            24.4  28.6   47.8  51.6    103   108   226  210
+//      256            24.9  39.2   49.9  77.6    119   154   310  278
+//     1024            35.3  74.2   83.2   142    224   292   702  581
+// (4 choices of rows of 4096: up to 256 chunks by each always, 359 and 364 us
+// with 8 experts, 469 and 558 with 1024.)
+constexpr int kMoeChunks = 256;
+
 template <int THR>
 __global__ __launch_bounds__(THR)
 void mx_moe_count(MoeArgs p)

@@ -83,7 +83,7 @@ int run_dispatch(const void *x, const int64_t *ids, int64_t tokens, int64_t top_
     a.each = plan.each;
     a.chunk = plan.chunk;
     a.chunks = plan.chunks;
-    a.summed = plan.chunks > 64;
+    a.summed = plan.chunks > kMoeChunks;
     a.per_row = fast_div((unsigned)(K / 8));
     // a few tokens' rows are shared by workgroups of 256 pieces
     a.segments = (int)std::max<int64_t>(1, std::min(cdiv(K / 8, 256), 256 / std::max<int64_t>(tokens, 1)));

@@ -1,6 +1,7 @@
 """GPU: mx_moe_combine_grad where two assignments name one row: the weights'
 gradients, the other rows and the memory behind them are as ever, and
-mx_moe_combine takes such rows as any."""
+mx_moe_combine takes such rows as any.  And mx_moe_dispatch around the number of
+chunks that its workgroups add up."""
 from __future__ import annotations
 
 import numpy as np
@@ -52,3 +53,9 @@ def test_combine_of_rows_that_are_named_twice():
     want, size = base.combined(y, pos, w)
     got = sr.f64(mx.moe_combine(y, pos, w, torch.float32))
     assert (np.abs(got - want) <= size * 4 * 2.0 ** -24 * 1.01).all()
+
+
+@pytest.mark.parametrize("tokens", [16384, 32767, 32768, 32769, 33000])
+def test_dispatch_at_the_most_chunks_that_each_workgroup_adds_up(tokens):
+    base.check_dispatch(tokens, 8, 40, 32)
+    base.check_dispatch(tokens * 8, 1, 1024, 32, "bf16")
