@@ -28,9 +28,21 @@ struct MoePlan {
 MoePlan moe_plan(int64_t tokens, int64_t top_k, int64_t groups)
 {
     MoePlan p = {};
-    // (as many tokens per workgroup as leave 1024 of them, four per CU: 8191
-    // tokens 31.6 us, in 2048 workgroups 33.7, in 512 34.6; 2048 with 8 choices
-    // 14.9, 18.2 and 15.2)
+    // As few tokens per workgroup as leave no more than 1024 workgroups, four per
+    // CU, whose loads are all in flight (so 513 to 1024 of them for 1025 tokens
+    // and more), and at most 64 assignments, past which there are more.  us on the
+    // GPU, 4 choices of rows of 4096 into E4M3 / 8 choices of rows of 2048, by
+    // tokens per workgroup:
+    //     tokens         1            2            3            4            8
+    //       1024    14.5  11.9   14.7  12.7   16.0  13.7   16.5  14.1
+    //       1025    14.1  12.1   14.3  12.6   15.3  13.6   16.5  14.1
+    //       1300    15.6  13.5   15.4  13.8   16.3  14.5   17.4  15.4
+    //       1800    19.0  20.0   15.8  16.3   18.4  16.1   16.8  17.2   21.0  20.6
+    //       2048    20.4  19.4   16.1  15.7   18.2  15.7   17.0  16.1   21.3  19.4
+    //       4096    30.0  29.5   28.2  27.4   27.4  22.5   26.2  22.3   27.8  23.6
+    //       8191    54.0  57.1   51.2  48.9   49.1  46.0   49.2  48.0   49.5  44.2
+    // (2 choices of rows of 4096: 1100 tokens 11.6 and 10.8, 1800 19.4 and 15.1;
+    // 9000 tokens of 4 choices, 8 per workgroup 58.4 and 4 54.2.)
     p.each = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(tokens, 1024), kMoeTopK / top_k));
     const int64_t total = tokens * top_k;
     // Up to 4096 assignments every workgroup goes through all of them (512
