@@ -16,14 +16,19 @@
 // m and the sums are FP32.  p is rounded to BF16 as the second product's
 // operand (half a step: 2^-8 of each p): values need BF16's range (FP16 would
 // lose a block whose scale is far from the others'), and a BF16 output is
-// rounded as coarsely itself: relative to 64 bits it is off by 0.0020 to 0.0023,
-// where its own rounding makes 0.0017 (2-norms over a call's outputs).  The FP16 and
-// FP32 outputs of trees (P2) take p in two parts, BF16(p) and BF16 of the rest,
-// with a second MFMA each: 2^-16 of each p, and FP32 outputs off by 2e-6 instead
-// of 0.0011 to 0.0016.  It costs nothing where loads and joins bound a call, and a third
-// where the MFMAs do (us, BF16 and FP32 outputs: 27 nodes over 1051 keys 12.7
-// and 12.8, 32 ragged trees 75 and 80, 24 under a window 24.1 and 26.4, two over
-// 131072 and 80868 keys 400 and 538).  The sum of the p's takes them unrounded.
+// rounded as coarsely itself: over a call's outputs it is off by 0.0020 to
+// 0.0023 of them, 2-norms, where its own rounding makes 0.0017.  The sum of the
+// p's takes them unrounded.
+//
+// Trees (P2) take p in two parts, BF16(p) and BF16 of the rest, with a second
+// MFMA each, within 2^-16 of each p: for FP16 and FP32 outputs, which are then
+// off by 2e-6 in FP32 instead of 0.0011 to 0.0016, and in tiles of 16 rows for
+// BF16 ones too.  There loads and joins are what bounds a call, and so few rows
+// do not average what a p is off by (one row over 7728 keys 0.0028).  us with one
+// part and with two, tiles of 16 rows: 27 nodes over 1051 keys 12.8 and 12.95, 32
+// sequences of 4 over 4096 57.6 and 57.8, 64 of 2 over 8000 in E2M1 102 and 106.
+// The tiles of more rows: 32 ragged trees 75 and 80, 24 under a window 24.1 and
+// 26.4, two over 131072 and 80868 keys, where MFMAs bound it, 400 and 538.
 //
 // The rows of one KV head.  All G = q_heads / kv_heads query heads of a KV
 // head read the same keys, so a tile's rows are (token, head of the group)

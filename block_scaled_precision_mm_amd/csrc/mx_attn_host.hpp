@@ -47,7 +47,8 @@ template <int F, int D, int PAGED, int TREE, int P2>
 AttnFn attn_fn(int which)
 {
     switch (which) {
-    case ROWS_16: return &mx_attn_rows<F, D, 1, PAGED, TREE, P2>;
+    // (trees: weights in two parts for every output, as it costs these next to nothing)
+    case ROWS_16: return &mx_attn_rows<F, D, 1, PAGED, TREE, TREE ? 1 : P2>;
     case ROWS_32: return &mx_attn_rows<F, D, 2, PAGED, TREE, P2>;
     case ROWS_128: return &mx_attn_tile<F, D, 4, PAGED, TREE, P2>;
     default: return &mx_attn_tile<F, D, 8, PAGED, TREE, P2>;
@@ -289,7 +290,8 @@ int run_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, 
         a.per_target = (float)a.heads / (float)plan.target[i];
         a.resident = plan.resident;
         const int64_t grid = plan.base[i] + (parts ? plan.target[i] : 0);
-        // (weights in two parts where the output has more bits than BF16)
+        // (weights in two parts where the output has more bits than BF16;
+        // tiles of 16 rows in any case)
         AttnFn fn = attn_fn<TREE, 0>(which, cache->is_fp4 != 0, cache->head_dim, cache->page_size);
         if constexpr (TREE)
             if (out_dtype != MXG_OUT_BF16)

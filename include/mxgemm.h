@@ -549,10 +549,10 @@ int mx_rope_cache_write(const mxg_kv_cache_t *cache, const void *q, void *q_out,
  *
  * All else, errors included, as for mx_paged_attention (NaN and infinities in
  * the values of a node that a row does not see do not reach it), but that p is
- * rounded to BF16 for BF16 outputs only: for FP16 and FP32 ones it is taken in
- * two BF16 parts, within 2^-16 of each p (up to a third slower where the
- * products bound the call); and MXG_ERR_NULL and MXG_ERR_PTR_ALIGN for the mask,
- * MXG_ERR_SHAPE for mask_words.
+ * rounded to BF16 for BF16 outputs only, and not for few rows: for FP16 and FP32
+ * ones, up to a third slower where the products bound the call, and where row
+ * tiles are of 16 rows it is taken in two BF16 parts, within 2^-16 of each p; and
+ * MXG_ERR_NULL and MXG_ERR_PTR_ALIGN for the mask, MXG_ERR_SHAPE for mask_words.
  */
 int mx_tree_attention(const mxg_kv_cache_t *cache, const void *q, int64_t q_stride, const int32_t *ends,
                       const int32_t *lens, const int32_t *table, int64_t table_width, const uint64_t *mask,

@@ -1,5 +1,6 @@
 """GPU: mx_tree_attention's FP32 and FP16 outputs, whose weights p are not rounded to
-BF16 but taken in two BF16 parts: within bounds that the rounded ones miss."""
+BF16 but taken in two BF16 parts: within bounds that the rounded ones miss.  In
+tiles of 16 rows BF16 outputs have them too."""
 from __future__ import annotations
 
 import numpy as np
@@ -75,3 +76,13 @@ def test_long_contexts_whole_and_in_parts(rows, dtype):
     c, most = make(case)
     c.check("by %d rows" % rows, max_new=most, dtype=dtype)
     c.check("whole by %d rows" % rows, max_new=most, dtype=dtype, workspace=None)
+
+
+@pytest.mark.parametrize("fmt,dim", FORMATS)
+def test_bf16_outputs_of_few_rows_are_the_fp32_ones_rounded_once(fmt, dim):
+    for case in (tc.SHORT[16], tc.LONG[16], tc.WINDOWED[16]):
+        c, most = make(case, fmt, dim)
+        for window in (0, 70):
+            wide, _ = c.run(window=window, max_new=most)
+            half, _ = c.run(dtype=torch.bfloat16, window=window, max_new=most)
+            assert torch.equal(half, wide.bfloat16())
