@@ -61,13 +61,15 @@
 // and of the new keys, its nodes, those of their mask's bits.  So only tiles
 // that hold a node, the last of a sequence, look at masks: a word or two per
 // row and tile, in the branch that other partly seen tiles take; the rest is
-// the same loop.  Bound as it: one tree of 27 nodes over 1051 keys 12.6 us (the
+// the same loop.  Bound as it: one tree of 27 nodes over 1051 keys 12.9 us (the
 // chain of dependent loads and the join of the parts), 32 of 16 over 100 to
-// 16000 keys, 64 rows a KV head, 75 us (239 MB, 3.2 TB/s; every key expanded
-// for two row tiles, VALU and MFMA issue), two of 488 and 320 rows over 131072
-// and 81000 keys in E2M1 384 to 404 us (0.95 PFLOP/s).  A tree's launch has one
-// kernel for all rows; its parts are chosen so that items run at once
-// (one_round), as there are too few rows for many rounds.
+// 16000 keys, 64 rows a KV head, 75 to 78 us (239 MB, 3.1 TB/s; every key is
+// expanded for two row tiles: VALU busy for 35% and MFMA for 16% of the SIMDs'
+// cycles, and 68% of the two waves that a SIMD has room for there, as items are
+// unequal), two of 488 and 344 rows over 131072 and 80868 keys in E2M1 387 to 401
+// us (0.94 to 0.97 PFLOP/s; VALU 42%, MFMA 49%).  A tree's launch has one kernel
+// for all rows; its parts are chosen so that items run at once (one_round), as
+// there are too few rows for many rounds.
 //
 // Masked places.  Scores of unseen keys are replaced, never added to;
 // values of slots past the sequence's end or on pages outside the cache are
@@ -224,13 +226,15 @@ __device__ __forceinline__ int cdiv_u(int a, int b) { return (int)(((unsigned)a 
 // Trees: the smallest chunk, from `least` on, with which all items run at
 // once.  (Chunks of the average work make up to one item per row tile more
 // than run at once, and those few are a second round: two sequences of 61 and
-// 40 nodes over 131072 and 81000 keys, 272 items of 256 rows for 256
+// 43 nodes over 131072 and 80868 keys, 272 items of 256 rows for 256
 // workgroups, took 650 us, and in one round 400.)  Where the row tiles alone are
 // too many for that, or it would leave the workgroups half idle: the average
 // work, which cuts none of like sequences, or 1.3 times that where some sequence
 // has far more: there the long ones' items go first (plan_item), so that short
 // ones fill the end (32 sequences of 100 to 16000 keys 77 us; with the average
-// work 89, twice that 83, half of it in the sequences' order 92).
+// work 89, twice that 83, half of it in the sequences' order 92).  More than 64
+// sequences, which a wave does not hold at once, have the average work and
+// their own order: 64 such sequences 141 us, 65 155, 128 285 (0.45, 0.45 and 0.91 GB).
 __device__ __forceinline__ int one_round(const AttnArgs &p, const AttnSeq &q, float total, int least)
 {
     if (p.seqs > 64)

@@ -162,6 +162,12 @@ AttnPlan attn_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
 //     32 of 64 over 100                          54    49    28    30
 //     32 of 64 over 1000                        119    89    60    57
 //     8 of 200 over 300                          67    61    44    39
+// The thresholds lie between these; near them the rule gives away up to 13%: 1 of
+// 117 nodes with 5 query heads each over 32691 keys, 4 KV heads, 56.5 us where
+// tiles of 128 take 49.9, 4 of 100 over 8000 43.9 and 38.8, 16 of 64 over 100 24.7
+// and 22.1.  And the keys are those that the table has room for, as lengths are on
+// the device: 27 nodes over 1051 keys take 13.0 us under a table of up to 4096 keys,
+// 14.8 under one of 16384 or 32768, 24.9 under one of 131072.
 AttnPlan tree_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, int64_t dim, int64_t max_new, int64_t keys)
 {
     AttnPlan p = {};
@@ -181,7 +187,10 @@ AttnPlan tree_plan(int64_t seqs, int64_t tokens, int64_t heads, int64_t group, i
     p.base[0] = heads * (rows / bm + some);
     // (with 768 instead of 512 the parts' joins cost more than the parts gain:
     // 1 sequence of 27 nodes over 16027 keys 40 us instead of 31; with 256, 1 of
-    // 200 over 4296 48 instead of 43)
+    // 200 over 4296 48 instead of 43.  Heads of 128; those of 64 have registers for
+    // three waves a SIMD in tiles of 32 rows and the same 512: 24 sequences of 1 to
+    // 200 nodes under a window of 1024, 476 row tiles of at most 11 key tiles, take
+    // 23 to 25 us, and took 22.5 with other settings)
     p.resident = p.which[0] == ROWS_256 ? 256 : 512;
     p.target[0] = p.resident;
     p.bytes[0] = p.base[0] <= kTreeTiles ? (size_t)2 * p.target[0] * attn_slot_bytes(bm, (int)dim) : 0;

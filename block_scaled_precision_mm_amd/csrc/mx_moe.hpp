@@ -11,11 +11,12 @@
 //   gradient   d_y[pos[t,j]] = w[t,j] d_out[t],  d_w[t,j] = <d_out[t], y[pos[t,j]]>
 //
 // All three are bound by HBM for many tokens: 8191 tokens of 4096 with 4 choices
-// each, half of them held here, into E4M3 137 MB in 31.6 us (4.3 TB/s, with the
-// kernel that counts), back from all of them 336 MB in 60 us (5.6 TB/s), the
-// gradients of 4095 with 2 choices 168 MB in 34 us (4.9 TB/s); and for a step's
-// few by the launch and a chain of dependent accesses: ids, counts, rows (64
-// tokens with 8 choices 4.6 and 3.2 us).
+// each, half of them held here, into E4M3 137 MB in 32 us (4.3 TB/s, with the
+// kernel that counts), back from all of them 336 MB in 63 us (5.3 TB/s), the
+// gradients of 4095 with 2 choices 168 MB in 34.5 us (4.9 TB/s), calls back to back
+// with inputs that change; and for a step's few by the launch and a chain of
+// dependent accesses: ids, counts, rows (64 tokens with 8 choices 4.7 and 2.7 us
+// in a replayed graph).
 #pragma once
 
 #include "mx_norm.hpp"
@@ -409,7 +410,9 @@ __device__ __forceinline__ float moe_weighted(float w, float v)
 
 // One workgroup per token: its row of d_out times each weight into d_y's rows,
 // and the products with y's summed over the row: in a thread's own order, then
-// over the lanes and the waves, in FP32.
+// over the lanes and the waves, in FP32.  Rows shorter than 2048 values leave some
+// of its threads without any: 4095 tokens with 2 choices, BF16, of 512 values 9.0
+// us for 21 MB, of 1024 11.4 for 42, of 2080 21.2 for 85, of 4096 34.5 for 168.
 template <int T, int OUT, int THR>
 __global__ __launch_bounds__(THR)
 void mx_moe_combine_grad_rows(CombineArgs p)
