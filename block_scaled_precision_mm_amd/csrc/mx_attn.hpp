@@ -1407,15 +1407,12 @@ void mx_attn_tile(AttnArgs p)
     // (0 for rows that are not there, whose scores are 0)
     float m = row.token >= 0 ? -__builtin_inff() : 0.0f, l = 0.0f;
     bf16x8v pb[4], rest[P2 ? 4 : 1];
-    auto clear_weights = [&] {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
-            if constexpr (P2)
-                rest[i] = pb[i];
-        }
-    };
-    clear_weights();
+    for (int i = 0; i < 4; ++i) {
+        pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
+        if constexpr (P2)
+            rest[i] = pb[i];
+    }
 
     // the loaded tile: this thread's chunks, and the keys that are there
     u4v codes[NI];
@@ -1676,7 +1673,12 @@ void mx_attn_tile(AttnArgs p)
         } else {
             // (p of a tile that no row of the wave sees; and said for x as well,
             // so that nothing keeps its registers through the other phase)
-            clear_weights();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pb[i] = as_bf16x8(u4v{0u, 0u, 0u, 0u});
+                if constexpr (P2)
+                    rest[i] = pb[i];
+            }
         }
         // (loads past the last tile are of page 0 of the cache and not used.
         // Under a condition the loop would wait for the loads it has just
