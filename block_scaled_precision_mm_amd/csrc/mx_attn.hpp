@@ -762,6 +762,48 @@ __device__ __forceinline__ void attn_sum_parts(const AttnArgs &p, const AttnItem
     }
 }
 
+// Parts first, first + step, .. below `end` of a row tile's n runs, by a
+// workgroup, each run's sums to put(run, sums).  Where the runs leave threads
+// over, two or four groups of threads take every second or fourth part each and
+// are joined in `scratch` (40 NTHR bytes of LDS).
+template <int D, int NR, int NTHR, class Put>
+__device__ __forceinline__ void attn_sum_runs(const AttnArgs &p, const AttnItem &it, int tid, int n, int first, int step, int end,
+                                              float *scratch, Put &&put)
+{
+    const int groups = n <= NTHR / 4 ? 4 : n <= NTHR / 2 ? 2 : 1;
+    if (groups > 1) {
+        // (whole waves per group: the first part is a scalar)
+        const int each = NTHR / groups, group = uniform(tid / each), i = tid - group * each;
+        AttnSums s;
+        if (i < n) {
+            attn_sum_parts<D, NR>(p, it, i, first + group * step, step * groups, end, s);
+            if (group > 0) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    scratch[e * NTHR + tid] = s.f[e];
+                scratch[8 * NTHR + tid] = s.m;
+                scratch[9 * NTHR + tid] = s.l;
+            }
+        }
+        __syncthreads();
+        if (group == 0 && i < n) {
+            for (int o = 1; o < groups; ++o) {
+                const float *src = scratch + o * each + i;
+                s.add({src[0], src[NTHR], src[2 * NTHR], src[3 * NTHR], src[4 * NTHR], src[5 * NTHR], src[6 * NTHR], src[7 * NTHR]},
+                      src[8 * NTHR], src[9 * NTHR]);
+            }
+            put(i, s);
+        }
+    } else {
+#pragma unroll 1
+        for (int i = tid; i < n; i += NTHR) {
+            AttnSums s;
+            attn_sum_parts<D, NR>(p, it, i, first, step, end, s);
+            put(i, s);
+        }
+    }
+}
+
 // Trees: the join of a row tile's parts, n runs of it, once this workgroup's
 // are in its slot: by the workgroup that arrives last.  More than 2 kJoin
 // parts are joined in two steps, kJoin of them by the last of each kJoin and
@@ -787,44 +829,12 @@ __device__ __forceinline__ void attn_join_tree(const AttnArgs &p, const AttnItem
     };
     // parts first, first + step, .. below end, to the outputs or to part `to`
     auto sum = [&](int first, int step, int end, int to) {
-        auto put = [&](int i, AttnSums &s) {
+        attn_sum_runs<D, NR, NTHR>(p, it, tid, n, first, step, end, scratch, [&](int i, AttnSums &s) {
             if (to < 0)
                 attn_write<D>(p, it, i, s);
             else
                 attn_put_part<D, NR>(attn_slot<D, NR>(p, it, to), i, s);
-        };
-        const int groups = n <= NTHR / 4 ? 4 : n <= NTHR / 2 ? 2 : 1;
-        if (groups > 1) {
-            // (whole waves per group)
-            const int each = NTHR / groups, group = uniform(tid / each), i = tid - group * each;
-            AttnSums s;
-            if (i < n) {
-                attn_sum_parts<D, NR>(p, it, i, first + group * step, step * groups, end, s);
-                if (group > 0) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        scratch[e * NTHR + tid] = s.f[e];
-                    scratch[8 * NTHR + tid] = s.m;
-                    scratch[9 * NTHR + tid] = s.l;
-                }
-            }
-            __syncthreads();
-            if (group == 0 && i < n) {
-                for (int o = 1; o < groups; ++o) {
-                    const float *src = scratch + o * each + i;
-                    s.add({src[0], src[NTHR], src[2 * NTHR], src[3 * NTHR], src[4 * NTHR], src[5 * NTHR], src[6 * NTHR], src[7 * NTHR]},
-                          src[8 * NTHR], src[9 * NTHR]);
-                }
-                put(i, s);
-            }
-        } else {
-#pragma unroll 1
-            for (int i = tid; i < n; i += NTHR) {
-                AttnSums s;
-                attn_sum_parts<D, NR>(p, it, i, first, step, end, s);
-                put(i, s);
-            }
-        }
+        });
     };
     if (it.parts <= 2 * kJoin) {
         if (last(it.counter, it.parts))
@@ -849,10 +859,9 @@ __device__ __forceinline__ void attn_join_tree(const AttnArgs &p, const AttnItem
 //
 // That workgroup reads the parts alone, one memory latency after the other,
 // which for one sequence's few rows cost more than the keys (4 rows of 64
-// parts 30 of 64 us): so parts hold only the rows that are there, and where
-// these leave threads over, two or four groups of threads take every second
-// or fourth part each and are joined in `scratch` (40 NTHR bytes of LDS that
-// nothing else uses any more).
+// parts 30 of 64 us): so parts hold only the rows that are there, and several
+// groups of threads share them (attn_sum_runs; `scratch`: LDS that nothing else
+// uses any more).
 template <int D, int NR, int NTHR, int TREE, class Get>
 __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &it, int tid, float *scratch, Get &&get)
 {
@@ -883,38 +892,7 @@ __device__ __forceinline__ void attn_finish(const AttnArgs &p, const AttnItem &i
     __syncthreads();
     if (arrived != (unsigned)(it.parts - 1))
         return;
-    const int groups = n <= NTHR / 4 ? 4 : n <= NTHR / 2 ? 2 : 1;
-    if (groups > 1) {
-        // (whole waves per group: `first` is a scalar)
-        const int each = NTHR / groups, group = uniform(tid / each), i = tid - group * each;
-        AttnSums s;
-        if (i < n) {
-            attn_sum_parts<D, NR>(p, it, i, group, groups, it.parts, s);
-            if (group > 0) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    scratch[e * NTHR + tid] = s.f[e];
-                scratch[8 * NTHR + tid] = s.m;
-                scratch[9 * NTHR + tid] = s.l;
-            }
-        }
-        __syncthreads();
-        if (group == 0 && i < n) {
-            for (int o = 1; o < groups; ++o) {
-                const float *src = scratch + o * each + i;
-                s.add({src[0], src[NTHR], src[2 * NTHR], src[3 * NTHR], src[4 * NTHR], src[5 * NTHR], src[6 * NTHR], src[7 * NTHR]},
-                      src[8 * NTHR], src[9 * NTHR]);
-            }
-            attn_write<D>(p, it, i, s);
-        }
-    } else {
-#pragma unroll 1
-        for (int i = tid; i < n; i += NTHR) {
-            AttnSums s;
-            attn_sum_parts<D, NR>(p, it, i, 0, 1, it.parts, s);
-            attn_write<D>(p, it, i, s);
-        }
-    }
+    attn_sum_runs<D, NR, NTHR>(p, it, tid, n, 0, 1, it.parts, scratch, [&](int i, AttnSums &s) { attn_write<D>(p, it, i, s); });
     if (tid == 0)
         __hip_atomic_store(p.counters + it.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
