@@ -66,8 +66,8 @@
 // 16000 keys, 64 rows a KV head, 75 to 78 us (239 MB, 3.1 TB/s; every key is
 // expanded for two row tiles: VALU busy for 35% and MFMA for 16% of the SIMDs'
 // cycles, and 68% of the two waves that a SIMD has room for there, as items are
-// unequal), two of 488 and 344 rows over 131072 and 80868 keys in E2M1 387 to 401
-// us (0.94 to 0.97 PFLOP/s; VALU 42%, MFMA 49%).  A tree's launch has one kernel
+// unequal), two of 488 and 344 rows over 131072 and 80868 keys in E2M1 387 to 415
+// us (0.91 to 0.97 PFLOP/s; VALU 42%, MFMA 49%).  A tree's launch has one kernel
 // for all rows; its parts are chosen so that items run at once (one_round), as
 // there are too few rows for many rounds.
 //
